@@ -447,9 +447,12 @@ int mil_ssm_token_logprobs(const void *logits, int32_t rows, int32_t vocab, int6
  * are added up); q: the student's probabilities.  Without MIL_DISTILL_TAIL p is divided by
  * its sum; with it everything outside the alternatives is one more outcome, with
  * p_t = max(0, 1 - sum p) and q_t = the rest of q:
- *   loss[r]     = sum p log(p / q)  (+ p_t log(p_t / q_t), where both are above 0)
+ *   loss[r]     = sum p log(p / q)  (+ p_t log(p_t / q_t), where p_t is above 0 and some logit
+ *                 outside the alternatives is above -inf)
  *   dlogits[r]  = grad_loss[r] / T * (q_i - p_i)             at the alternatives
  *                 grad_loss[r] / T * q_i (1 - p_t / q_t)     elsewhere (q_i without the tail)
+ * Both hold however far the rest of q lies below the alternatives: a finite logit counts with its
+ * value, the type's lowest included; -inf alone is a mask.
  * A row with no alternative (padding; also when every p is 0) has loss 0 and gradient 0 whatever
  * its logits hold; an id outside the vocabulary, or a NaN log probability of an id that is
  * present, makes the row's loss and gradient NaN.  A student that masks an alternative (q = 0

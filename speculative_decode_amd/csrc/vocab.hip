@@ -461,10 +461,16 @@ __global__ __launch_bounds__(kNT) void logprob_join(const LogprobParams p) {
 // q: the student's.  With the tail, everything else is one more outcome with p_t = 1 - sum p
 // and q_t = sum of q outside the alternatives; without, p is divided by its sum.
 //   loss       = sum p log(p/q) (+ p_t log(p_t/q_t))
-//   dloss/dz_i = (q_i - p_i)/T at the alternatives,  q_i (1 - p_t/q_t)/T (or q_i/T) elsewhere
-// q_t is summed directly, never as 1 - sum q.  The alternatives are few: lane q of every wave
-// knows where alternative q lies (which vector, of which wave and lane), and a wave that
-// comes to a vector asks by one ballot whether there are any in its 64; one in four has.
+//   dloss/dz_i = (q_i - p_i)/T at the alternatives,  (q_i - p_t q_i/q_t)/T (or q_i/T) elsewhere
+// What lies outside the alternatives is summed directly, never as 1 - sum q, and relative to its
+// own greatest logit m_r: with r_i = e^{(z_i - m_r)/T} and R = sum r_i there,
+//   log q_t = (m_r - m)/T + log R - log Z,    gradient there = r_i ((q_t - p_t)/R)/T
+// hold however far it lies below the alternatives (relative to the row's maximum it is 0 in fp32
+// from 87 T down): no factor is above 1, and -inf gives 0.
+// The alternatives are few: lane q of every wave knows where alternative q lies (which vector,
+// of which wave and lane), and a wave that comes to a vector asks by one ballot whether there
+// are any in its 64; one in four has.  They are taken out of the vectors (-inf in their place)
+// before anything is summed.
 struct DistillParams {
     const void *logits;
     int64_t stride;
@@ -473,8 +479,8 @@ struct DistillParams {
     const int32_t *ids;
     const float *lp;
     float *loss;
-    float4 *part;   // [rows][S]: maximum, sum over the alternatives, sum elsewhere
-    float4 *stats;  // [rows]: maximum, 1/S, slope outside the alternatives, 1 or 0 (no alternatives)
+    float4 *part;   // [rows][S]: outside the alternatives, the maximum and the sum relative to it
+    float4 *stats;  // [rows]: maximum outside, (q_t - p_t)/R, the row's maximum, 1/Z (-1: no alternatives)
     const float *grad;
     void *out;
     int64_t out_stride;
@@ -511,20 +517,29 @@ __device__ __forceinline__ Teacher teacher(const DistillParams &a, int64_t row, 
     if (later) t.id = -1;  // the first of a repeated id stands for all
     return t;
 }
-// Loss and slope of a row from its sums: e^{(z-m)/T} over the alternatives and elsewhere.
-__device__ __forceinline__ void row_loss(const DistillParams &a, const Teacher &t, float zj, float m, double top,
-                                         double rest, float &loss, float &slope) {
-    const double Z = top + rest;  // 0: the student's row is masked whole, every q is 0
-    const double logq = Z == 0.0 ? -(double)INFINITY : ((double)zj - (double)m) / (double)a.T - log(Z);
-    double l = t.p > 0.0 ? t.p * (log(t.p) - logq) : 0.0;
+// What a row's loss and gradient are made of
+struct RowEnd {
+    float loss, m, slope;  // slope: of the gradient outside the alternatives, (q_t - p_t)/R
+    double Z;              // sum of e^{(z-m)/T} over the whole row (0: all of it is masked)
+};
+// From the greatest logit outside the alternatives, R = sum of e^{(z-m_r)/T} there, and each lane's
+// own alternative's logit.  A NaN or +inf anywhere makes Z a NaN, and with it everything.
+__device__ __forceinline__ RowEnd row_end(const DistillParams &a, const Teacher &t, float zj, float mr, double R) {
+    RowEnd o;
+    o.m = fmaxf(mr, wave_max(t.id >= 0 ? zj : -INFINITY));
+    if (o.m == -INFINITY) o.m = 0.f;
+    const double T = (double)a.T, dj = ((double)zj - (double)o.m) / T, below = ((double)mr - (double)o.m) / T;
+    const double rest = R == 0.0 ? 0.0 : R * exp(below);
+    // (fp32 will do: an argument's rounding, 2^-24 |d| of e^d, is largest at d = -1)
+    o.Z = (double)wave_sum(t.id >= 0 ? expf((float)dj) : 0.f) + rest;
+    const double pt = a.tail ? fmax(0.0, 1.0 - t.total) : 0.0;
+    o.slope = (float)(R == 0.0 ? 0.0 * o.Z : (rest / o.Z - pt) / R);
+    // p log(p/q) = p (log(p Z) - (z-m)/T), and so for the tail
+    double l = t.p > 0.0 ? (o.Z == 0.0 ? (double)INFINITY : t.p * (log(t.p * o.Z) - dj)) : 0.0;
     l = wave_sum(l);
-    slope = 1.f;
-    if (a.tail) {
-        const double pt = fmax(0.0, 1.0 - t.total), qt = rest / Z;
-        if (pt > 0.0 && qt > 0.0) l += pt * log(pt / qt);
-        slope = qt > 0.0 ? (float)(1.0 - pt / qt) : 0.f;
-    }
-    loss = (float)l;
+    if (pt > 0.0 && R > 0.0) l += pt * (log(pt * o.Z / R) - below);
+    o.loss = (float)l;
+    return o;
 }
 
 // Where this lane's alternative lies among the vectors of a workgroup with STEP threads (vector
@@ -574,26 +589,34 @@ __device__ __forceinline__ float exp_of(float z, float m, const Scale &c) {
     return __builtin_amdgcn_exp2f(fmaf(d, c.lo, d * c.hi));
 }
 
-// Sums of one vector: e at the alternatives goes to `top`, the rest is returned
+// -inf in the place of the alternatives in vector j
 template <bool BF>
-__device__ __forceinline__ float sum_vec(u32x4 raw, const Spot &spot, int j, float m, const Scale &c, float &top) {
+__device__ __forceinline__ void take_out(u32x4 &raw, const Spot &spot, int j) {
+    constexpr int EPV = Vec<BF>::EPV;
+    at_spots(spot, j, [&](int, int place, bool mine) {
+#pragma unroll
+        for (int i = 0; i < EPV; ++i)
+            if (place == i) {
+                constexpr int per = BF ? 2 : 1;
+                const uint32_t w = raw[i / per];
+                const uint32_t out = !BF ? 0xff800000u : i % per ? (w & 0xffffu) | 0xff800000u : (w & 0xffff0000u) | 0xff80u;
+                raw[i / per] = mine ? out : w;
+            }
+    });
+}
+// Sum of one vector
+template <bool BF>
+__device__ __forceinline__ float sum_vec(u32x4 raw, float m, const Scale &c) {
     constexpr int EPV = Vec<BF>::EPV;
     float f[EPV];
     Vec<BF>::unpack(raw, f);
 #pragma unroll
     for (int i = 0; i < EPV; ++i) f[i] = exp_of(f[i], m, c);
-    at_spots(spot, j, [&](int, int place, bool mine) {
-#pragma unroll
-        for (int i = 0; i < EPV; ++i)
-            if (place == i) {
-                top += mine ? f[i] : 0.f;
-                f[i] = mine ? 0.f : f[i];  // (a repeated id finds 0)
-            }
-    });
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < EPV; ++i) sum += f[i];
     asm volatile("" : "+v"(sum));  // now: put off to where the sum is used, the terms of all vectors would wait
+    __builtin_amdgcn_sched_barrier(0);  // and one vector after another, for the same reason
     return sum;
 }
 
@@ -602,22 +625,25 @@ __device__ __forceinline__ float sum_vec(u32x4 raw, const Spot &spot, int j, flo
 template <bool BF, int VPT>
 __global__ __launch_bounds__(kNT, 4) void distill_slice(const DistillParams p) {
     constexpr int EPV = Vec<BF>::EPV;
-    __shared__ float sMax[4], sSum[4][2];
+    __shared__ float sMax[4], sSum[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t item = blockIdx.x;
     const int64_t row = item / p.S;
     const int s = (int)(item - row * p.S);
     const Row r = open_row<BF>(p.logits, row, p.stride, p.V);
     const int v0 = s * p.vps, v1 = min(v0 + p.vps, r.nv);
+    // (asked for first: the vectors are looked at as they arrive, which takes the alternatives)
+    const int id = lane < p.k ? p.ids[row * p.k + lane] : -1;
     u32x4 raw[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = v0 + j * kNT + tid;
         raw[j] = v < v1 ? load_vec<BF>(r, v) : no_vec<BF>();
     }
-    const int id = lane < p.k ? p.ids[row * p.k + lane] : -1;
     const Spot spot = spot_of<EPV, kNT>(id < p.V ? id : -1, r.off, v0, v1, wave);
     float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) take_out<BF>(raw[j], spot, j);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         float f[EPV];
@@ -631,17 +657,14 @@ __global__ __launch_bounds__(kNT, 4) void distill_slice(const DistillParams p) {
     m = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
     const float mm = m == -INFINITY ? 0.f : m;
     const Scale c = scale_of(p.T);
-    float top = 0.f, rest = 0.f;
+    float rest = 0.f;
     again(raw);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) rest += sum_vec<BF>(raw[j], spot, j, mm, c, top);
-    top = wave_sum(top);
+    for (int j = 0; j < VPT; ++j) rest += sum_vec<BF>(raw[j], mm, c);
     rest = wave_sum(rest);
-    if (lane == 0) sSum[wave][0] = top, sSum[wave][1] = rest;
+    if (lane == 0) sSum[wave] = rest;
     __syncthreads();
-    if (tid == 0)
-        p.part[item] = make_float4(m, (sSum[0][0] + sSum[1][0]) + (sSum[2][0] + sSum[3][0]),
-                                   (sSum[0][1] + sSum[1][1]) + (sSum[2][1] + sSum[3][1]), 0.f);
+    if (tid == 0) p.part[item] = make_float4(m, (sSum[0] + sSum[1]) + (sSum[2] + sSum[3]), 0.f, 0.f);
 }
 
 // Loss of a row from its slices: one wave per row.  6 us for 515 rows.
@@ -653,24 +676,19 @@ __global__ __launch_bounds__(kNT) void distill_join(const DistillParams p) {
     const Teacher t = teacher(p, row, lane);
     float m = -INFINITY;
     for (int s = 0; s < p.S; ++s) m = fmaxf(m, p.part[row * p.S + s].x);
-    double top = 0.0, rest = 0.0;
+    double R = 0.0;
     for (int s = 0; s < p.S; ++s) {
         const float4 q = p.part[row * p.S + s];
-        if (q.x == -INFINITY && q.y == 0.f && q.z == 0.f) continue;
-        const double f = exp(((double)q.x - (double)m) / (double)p.T);
-        top += f * (double)q.y;
-        rest += f * (double)q.z;
+        if (q.x == -INFINITY && q.y == 0.f) continue;  // nothing in this slice
+        R += exp(((double)q.x - (double)m) / (double)p.T) * (double)q.y;
     }
     const Row r = open_row<BF>(p.logits, row, p.stride, p.V);
-    const float zj = t.id >= 0 ? row_elt<BF>(r, t.id) : 0.f;
-    float loss, slope;
-    row_loss(p, t, zj, m == -INFINITY ? 0.f : m, top, rest, loss, slope);
+    const RowEnd o = row_end(p, t, t.id >= 0 ? row_elt<BF>(r, t.id) : 0.f, m, R);
     if (lane == 0) {
         const float nan = __uint_as_float(0x7fc00000u);
-        p.loss[row] = t.bad ? nan : t.any ? loss : 0.f;
-        const double Z = top + rest;
-        p.stats[row] = make_float4(m == -INFINITY ? 0.f : m, Z == 0.0 ? 0.f : (float)(1.0 / Z), slope,
-                                   t.bad ? nan : t.any ? 1.f : 0.f);
+        p.loss[row] = t.bad ? nan : t.any ? o.loss : 0.f;
+        p.stats[row] = make_float4(m == -INFINITY ? 0.f : m, t.bad ? nan : o.slope, o.m,
+                                   t.bad ? nan : !t.any ? -1.f : o.Z == 0.0 ? 0.f : (float)(1.0 / o.Z));
     }
 }
 
@@ -693,26 +711,29 @@ __device__ __forceinline__ void store_vec(char *orow, int ooff, int off, int V, 
             reinterpret_cast<uint32_t *>(orow)[e] = w[i];
     }
 }
-// Gradient of one vector of logits.  w: the row's incoming gradient over T; pj: p of this lane's
-// alternative.  (Here the constant in one part will do: it moves a probability by no more
-// than its own argument's rounding.)
-template <bool BF>
-__device__ __forceinline__ void grad_vec(u32x4 raw, const Spot &spot, int j, float pj, float m, float c, float w,
-                                         float wq, float wqs, float (&g)[Vec<BF>::EPV]) {
+// Gradient of one vector of logits: wr e^{(z-m)c}, m the maximum outside the alternatives, and
+// own(q, z) at alternative q.  (Here the constant in one part will do: it moves a probability by
+// no more than its own argument's rounding.)
+template <bool BF, typename F>
+__device__ __forceinline__ void grad_vec(u32x4 raw, const Spot &spot, int j, float m, float c, float wr, F own,
+                                         float (&g)[Vec<BF>::EPV]) {
     constexpr int EPV = Vec<BF>::EPV;
     float f[EPV];
     Vec<BF>::unpack(raw, f);
 #pragma unroll
-    for (int i = 0; i < EPV; ++i) {
-        f[i] = __builtin_amdgcn_exp2f((f[i] - m) * c);
-        g[i] = f[i] * wqs;
-    }
+    for (int i = 0; i < EPV; ++i) g[i] = __builtin_amdgcn_exp2f((f[i] - m) * c) * wr;
     at_spots(spot, j, [&](int q, int place, bool mine) {
-        const float v = w * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pj), q));
 #pragma unroll
         for (int i = 0; i < EPV; ++i)
-            if (place == i) g[i] = mine ? f[i] * wq - v : g[i];
+            if (place == i) {
+                const float v = own(q, f[i]);
+                g[i] = mine ? v : g[i];
+            }
     });
+}
+// The value of one lane, the same for all
+__device__ __forceinline__ float of_lane(float v, int q) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), q));
 }
 
 template <bool BF, int VPT>
@@ -742,15 +763,18 @@ __global__ __launch_bounds__(kNT, 4) void distill_grad(const DistillParams p) {
     const float pj = sP[lane];
     const float4 st = p.stats[row];
     const float c = kLog2e / p.T;
-    const float w = p.grad[row] / p.T * st.w, wq = w * st.y, wqs = wq * st.z;
+    const float w = p.grad[row] / p.T, wq = w * st.w, wr = w * st.y, wp = w * pj;
     char *orow = static_cast<char *>(p.out) + row * p.out_stride * Vec<BF>::ELT;
     const int ooff = (int)((reinterpret_cast<uintptr_t>(orow) & 15) / Vec<BF>::ELT);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int q = j * kNT + tid;
         float g[EPV];
-        grad_vec<BF>(raw[j], spot, j, pj, st.x, c, w, wq, wqs, g);
-        if (st.w == 0.f) {  // no alternatives: zeros, whatever the logits hold
+        // (an alternative's logit as it was loaded: out may be the logits, and the workgroup of
+        // another slice through with them)
+        grad_vec<BF>(raw[j], spot, j, st.x, c, wr,
+                     [&](int q, float z) { return __builtin_amdgcn_exp2f((z - st.z) * c) * wq - of_lane(wp, q); }, g);
+        if (st.w < 0.f) {  // no alternatives: zeros, whatever the logits hold
 #pragma unroll
             for (int i = 0; i < EPV; ++i) g[i] = 0.f;
         }
@@ -769,6 +793,7 @@ __global__ __launch_bounds__(kNT, 4) void distill_grad(const DistillParams p) {
 struct RowTeacher {
     int id[64];
     float p[64], z[64];
+    float top;  // the greatest z
     double total;
     int kind;  // 0: no alternatives, 1: some, 2: an id behind the vocabulary or a NaN
 };
@@ -778,7 +803,7 @@ template <bool BF, int NW, int VPT>
 __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const DistillParams p) {
     constexpr int EPV = Vec<BF>::EPV, MW = NW - 1, NT = MW * 64;
     __shared__ RowTeacher sT[2];
-    __shared__ float sMax[MW], sSum[MW][2];
+    __shared__ float sMax[MW], sSum[MW];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nv = p.V / EPV;
     if (wave == MW) {
@@ -788,8 +813,10 @@ __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const D
             RowTeacher &o = sT[at];
             o.id[lane] = t.id;
             o.p[lane] = (float)t.p;
-            o.z[lane] = t.id >= 0 ? row_elt<BF>(open_row<BF>(p.logits, row, p.stride, p.V), t.id) : 0.f;
-            if (lane == 0) o.total = t.total, o.kind = t.bad ? 2 : t.any;
+            const float z = t.id >= 0 ? row_elt<BF>(open_row<BF>(p.logits, row, p.stride, p.V), t.id) : -INFINITY;
+            o.z[lane] = z;
+            const float top = wave_max(z);
+            if (lane == 0) o.top = top, o.total = t.total, o.kind = t.bad ? 2 : t.any;
         };
         prepare(blockIdx.x, 0);
         lds_barrier();
@@ -798,16 +825,10 @@ __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const D
             lds_barrier();
             lds_barrier();
             float m = -INFINITY;
-            double top = 0.0, rest = 0.0;
-            for (int i = 0; i < MW; ++i) {
-                m = fmaxf(m, sMax[i]);
-                top += (double)sSum[i][0];
-                rest += (double)sSum[i][1];
-            }
-            float loss, slope;
-            const bool bad = t.bad, any = t.any;
-            row_loss(p, t, sT[at].z[lane], m == -INFINITY ? 0.f : m, top, rest, loss, slope);
-            if (lane == 0) p.loss[row] = bad ? __uint_as_float(0x7fc00000u) : any ? loss : 0.f;
+            double R = 0.0;
+            for (int i = 0; i < MW; ++i) m = fmaxf(m, sMax[i]), R += (double)sSum[i];
+            const RowEnd o = row_end(p, t, sT[at].z[lane], m, R);
+            if (lane == 0) p.loss[row] = t.bad ? __uint_as_float(0x7fc00000u) : t.any ? o.loss : 0.f;
             if (row + gridDim.x < p.rows) prepare(row + gridDim.x, at ^ 1);
             lds_barrier();
         }
@@ -835,6 +856,8 @@ __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const D
         const Spot spot = spot_of<EPV, NT>(t.id[lane], 0, 0, nv, wave);
         float m = -INFINITY;
 #pragma unroll
+        for (int j = 0; j < VPT; ++j) take_out<BF>(raw[j], spot, j);
+#pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (j * NT + tid >= nv) continue;
             float f[EPV];
@@ -846,27 +869,30 @@ __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const D
         if (lane == 0) sMax[wave] = m;
         lds_barrier();
         for (int i = 0; i < MW; ++i) m = fmaxf(m, sMax[i]);
+        const float whole = fmaxf(m, t.top), mw = whole == -INFINITY ? 0.f : whole;
+        const float below = m == -INFINITY ? 0.f : exp_of(m, mw, c);
         m = m == -INFINITY ? 0.f : m;
-        float top = 0.f, rest = 0.f;
+        float rest = 0.f;
         again(raw);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const float sum = sum_vec<BF>(raw[j], spot, j, m, c, top);
+            const float sum = sum_vec<BF>(raw[j], m, c);
             rest += j * NT + tid < nv ? sum : 0.f;
         }
-        top = wave_sum(top);
         rest = wave_sum(rest);
-        if (lane == 0) sSum[wave][0] = top, sSum[wave][1] = rest;
+        if (lane == 0) sSum[wave] = rest;
+        const float own = exp_of(t.z[lane], mw, c), top = wave_sum(own);  // (0 where there is no alternative)
         lds_barrier();
-        double drest = 0.0, Z = 0.0;
+        double R = 0.0;
 #pragma unroll 1
-        for (int i = 0; i < MW; ++i) drest += (double)sSum[i][1], Z += (double)sSum[i][0];
-        Z += drest;
+        for (int i = 0; i < MW; ++i) R += (double)sSum[i];
+        // as in row_end (what `below` loses under 2^-126 is nothing beside what is added to it)
+        const double rw = R * (double)below, Z = (double)top + rw;
         const int kind = t.kind;
-        float slope = 1.f;
-        if (p.tail) slope = drest > 0.0 ? (float)(1.0 - fmax(0.0, 1.0 - t.total) * Z / drest) : 0.f;
+        const double pt = p.tail ? fmax(0.0, 1.0 - t.total) : 0.0;
         const float w = kind == 2 ? __uint_as_float(0x7fc00000u) : p.grad[row] / p.T;
-        const float wq = Z == 0.0 ? 0.f * w : (float)((double)w / Z), wqs = wq * slope;
+        const float wr = w * (float)(R == 0.0 ? 0.0 * Z : (rw / Z - pt) / R);
+        const float gq = own * (Z == 0.0 ? 0.f : (float)((double)w / Z)) - w * t.p[lane];
         const int64_t next = row + gridDim.x;
         const __amdgpu_buffer_rsrc_t out = view(p.out, row, p.out_stride);
         const __amdgpu_buffer_rsrc_t in = view(p.logits, next < p.rows ? next : row, p.stride);
@@ -874,7 +900,7 @@ __global__ __launch_bounds__(NW * 64, rows_waves(VPT)) void distill_rows(const D
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             float g[EPV];
-            grad_vec<BF>(raw[j], spot, j, t.p[lane], m, c1, w, wq, wqs, g);
+            grad_vec<BF>(raw[j], spot, j, m, c1, wr, [&](int q, float) { return of_lane(gq, q); }, g);
             u32x4 o = Vec<BF>::pack(g);
             if (kind == 0) o = (u32x4){};
             __builtin_amdgcn_raw_buffer_store_b128(o, out, tid * 16, j * NT * 16, 0);
