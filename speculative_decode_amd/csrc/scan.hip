@@ -383,14 +383,14 @@ __global__ __launch_bounds__(1024) void scan_grad(const ScanParams p) {
         if (t < k.len)
             for (int u = t; u < k.len; ++u) g += W[u][t];
         float later = t < k.len ? e : 0.f, before = t < k.len ? f * dts[t] : 0.f;
-        const float own = before;
 #pragma unroll
         for (int d = 1; d < kQ; d <<= 1) {
             const float x = __shfl_down(later, d), y = __shfl_up(before, d);
             if (t + d < kQ) later += x;
             if (t >= d) before += y;
         }
-        g += later + (before - own) + dot;
+        const float upto = __shfl_up(before, 1);  // without the token's own, whatever its size
+        g += later + (t > 0 ? upto : 0.f) + dot;
         if (t < have) put<BF>(p.ddt, (k.t0 + t) * p.H + k.h, t < k.len ? fmaf(p.A[k.h], g, col + f) : 0.f);
         sG[t] = t < k.len ? g * dts[t] : 0.f;
     }

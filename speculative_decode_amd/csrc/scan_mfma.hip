@@ -693,7 +693,6 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         const float r0 = m > 0 ? sm.row[0][u] : 0.f, r1 = m > 1 ? sm.row[1][u] : 0.f,
                     r2 = m > 2 ? sm.row[2][u] : 0.f;
         float rs = r0 + r1 + r2, cs = after * du;  // rows: suffix over the tile; columns: prefix before u
-        const float cown = cs;
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
             const float x = __shfl_down(rs, d), y = __shfl_up(cs, d);
@@ -701,17 +700,18 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
             if (c >= d) cs += y;
         }
         const float R0 = sum16(r0), R1 = sum16(r1);
+        const float cb = __shfl_up(cs, 1);  // without the token's own, whatever its size
         const float t20 = __shfl(R0, 32), t30 = __shfl(R0, 48), t31 = __shfl(R1, 48);
-        float g = sm.diag[u] + rs + (cs - cown) + (m == 1 ? t20 + t30 : m == 2 ? t30 + t31 : 0.f);
+        float g = sm.diag[u] + rs + (c > 0 ? cb : 0.f) + (m == 1 ? t20 + t30 : m == 2 ? t30 + t31 : 0.f);
         float later = e, before = f * du;
-        const float bown = before;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const float x = __shfl_down(later, d), y = __shfl_up(before, d);
             if (u + d < 64) later += x;
             if (u >= d) before += y;
         }
-        g += later + (before - bown) + decay * all;
+        const float bb = __shfl_up(before, 1);
+        g += later + (u > 0 ? bb : 0.f) + decay * all;
         const bool live = ch * kQ + u < w.live;
         dA += live ? (double)(g * du) : 0.0;
         if (u < have) {
