@@ -176,12 +176,14 @@ def topk_distill(logits, top_ids, top_logprobs, temperature=1.0, tail=True):
 def topk_distill_grad(logits, top_ids, top_logprobs, grad_loss, temperature=1.0, tail=True, out=None):
     """`topk_distill` and its gradient in one call, for a step that knows each row's weight:
     grad_loss [...] float32.  Returns (loss [...], dlogits [..., V]); `out` may supply dlogits
-    (rows evenly spaced), and may be the logits themselves, which are then overwritten.
+    (rows evenly spaced), and may be the logits themselves, which are then overwritten: as after
+    any in-place operation, a backward pass that needs their old values raises.
     No gradients are recorded."""
     what = "topk_distill_grad"
     rows, V, stride, k, dev, lead = _check_distill(what, logits, top_ids, top_logprobs)
     _side(what, "grad_loss", grad_loss, lead, torch.float32, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
         raise ValueError(f"{what}: out must be a {logits.dtype} tensor of shape {tuple(logits.shape)} on {dev}")
@@ -196,4 +198,6 @@ def topk_distill_grad(logits, top_ids, top_logprobs, grad_loss, temperature=1.0,
                                              addr(grad_loss), addr(loss), addr(out), ostride, ws, ws_bytes,
                                              stream(dev)),
                 "mil_ssm_distill_grad")
+    if given:  # so that a graph that has kept what was overwritten notices
+        torch.autograd.graph.increment_version(out)
     return loss, out

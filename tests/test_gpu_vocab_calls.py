@@ -1,0 +1,48 @@
+"""Calls of the operators over logits that concern their memory rather than their numbers."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from speculative_decode_amd import _lib as L
+from speculative_decode_amd import token_logprobs, topk_distill, topk_distill_grad
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    L.lib()
+
+
+def inputs(rows=4, V=1000, k=5, dt=F32):
+    gen = torch.Generator(device="cuda").manual_seed(rows + V)
+    z = torch.randn(rows, V, generator=gen, device="cuda").to(dt)
+    _, _, ids, top = token_logprobs(torch.randn(rows, V, generator=gen, device="cuda"), top_k=k)
+    return z, ids, top, torch.rand(rows, generator=gen, device="cuda")
+
+
+def test_logits_overwritten_in_place_are_noticed():
+    """a graph that has kept the logits must not go on with the gradient in their place"""
+    z, ids, top, g = inputs()
+    leaf = z.clone().requires_grad_(True)
+    soft = torch.tanh(leaf)  # keeps its own result for its gradient
+    topk_distill_grad(soft.detach(), ids, top, g, out=soft.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        soft.sum().backward()
+    leaf = z.clone().requires_grad_(True)
+    loss = topk_distill(leaf, ids, top)
+    topk_distill_grad(z, ids, top, g, out=leaf.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    # a result of the call's own making, and the logits' old values elsewhere, are no such thing
+    soft = torch.tanh(leaf)
+    topk_distill_grad(soft.detach(), ids, top, g)
+    topk_distill_grad(soft.detach(), ids, top, g, out=torch.empty_like(z))
+    soft.sum().backward()
+    with torch.inference_mode():
+        out = torch.empty_like(z)
+    topk_distill_grad(z, ids, top, g, out=out)
