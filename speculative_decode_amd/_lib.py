@@ -140,3 +140,9 @@ def status_string(status: int) -> str:
 def check(status: int, what: str) -> None:
     if status != MIL_OK:
         raise MilError(status, what)
+
+
+def check_sizes(what: str, *sizes) -> None:
+    """The library takes sizes in 32 bits; ctypes would cut larger ones to their lower half."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise MilError(MIL_E_UNSUPPORTED, what)

@@ -55,6 +55,7 @@ def _rows(what, t):
     V = int(t.shape[-1])
     if V < 1:
         raise ValueError(f"{what}: an empty vocabulary")
+    L.check_sizes(what, V, t.numel() // V)
     if t.is_contiguous():
         return t.numel() // V, V, V
     lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]

@@ -81,6 +81,7 @@ def ssm_scan(x, B, C, dt, A, D, h0=None, lengths=None):
         raise TypeError(f"ssm_scan: x must be float32 or bfloat16, got {x.dtype}")
     nseq, T, H, P = (int(n) for n in x.shape)
     G, N = int(B.shape[2]), int(B.shape[3])
+    L.check_sizes("ssm_scan", nseq, T, H, P, G, N)
     f32, tok, dev = torch.float32, x.dtype, x.device
     for name, t, shape, dtype in (("x", x, (nseq, T, H, P), tok), ("B", B, (nseq, T, G, N), tok),
                                   ("C", C, (nseq, T, G, N), tok), ("dt", dt, (nseq, T, H), tok), ("A", A, (H,), f32),

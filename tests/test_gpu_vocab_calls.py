@@ -46,3 +46,16 @@ def test_logits_overwritten_in_place_are_noticed():
     with torch.inference_mode():
         out = torch.empty_like(z)
     topk_distill_grad(z, ids, top, g, out=out)
+
+
+@pytest.mark.parametrize("rows,V", [(1, 2 ** 32 + 5), (2 ** 32 + 3, 1), (2 ** 31, 2)])
+def test_sizes_past_32_bits_are_refused(rows, V):
+    """not taken for what their lower 32 bits say"""
+    z = torch.empty(rows, V, dtype=BF, device="cuda")
+    with pytest.raises(L.MilError) as e:
+        token_logprobs(z, top_k=1)
+    assert e.value.status == L.MIL_E_UNSUPPORTED
+    few = torch.zeros(1, 1, dtype=torch.int32, device="cuda").expand(rows, 1)
+    with pytest.raises(L.MilError) as e:
+        topk_distill(z, few, few.float())
+    assert e.value.status == L.MIL_E_UNSUPPORTED
