@@ -671,6 +671,11 @@ static int check_distill_out(const void *logits, int32_t rows, int32_t vocab, in
     if (!aligned(grad_loss, 4) || !aligned(dlogits, eb)) return MIL_E_ALIGN;
     if (dlogits == logits) return out_stride == row_stride ? MIL_OK : MIL_E_INVALID;
     const char *a = static_cast<const char *>(logits), *b = static_cast<const char *>(dlogits);
+    if (out_stride == row_stride) {  // rows of one may lie between those of the other
+        const int64_t way = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / eb % row_stride;
+        const int64_t after = way < 0 ? way + row_stride : way;
+        if (after >= vocab && row_stride - after >= vocab) return MIL_OK;
+    }
     const int64_t la = ((rows - 1) * row_stride + vocab) * eb, lb = ((rows - 1) * out_stride + vocab) * eb;
     return (b >= a + la || a >= b + lb) ? MIL_OK : MIL_E_INVALID;
 }

@@ -59,3 +59,18 @@ def test_sizes_past_32_bits_are_refused(rows, V):
     with pytest.raises(L.MilError) as e:
         topk_distill(z, few, few.float())
     assert e.value.status == L.MIL_E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("V", [1000, 999])
+def test_gradient_beside_the_logits(dt, V):
+    """logits and gradient as the two halves of each row of one buffer"""
+    z, ids, top, g = inputs(V=V, dt=dt)
+    want = topk_distill_grad(z, ids, top, g)
+    wide = torch.zeros(4, 2 * V, dtype=dt, device="cuda")
+    wide[:, :V] = z
+    loss, d = topk_distill_grad(wide[:, :V], ids, top, g, out=wide[:, V:])
+    assert torch.equal(wide[:, :V], z) and torch.equal(wide[:, V:], d)
+    # (an odd row's other half begins off a 16-byte boundary, where the separate launches add up in another order)
+    assert (loss - want[0]).abs().max() <= 4e-5
+    assert (d.float() - want[1].float()).abs().max() <= 2 * torch.finfo(dt).eps * want[1].float().abs().max() + 1e-6
