@@ -412,7 +412,8 @@ int mil_ssm_scan_backward(const mil_ssm_dims *dims, int32_t T, int32_t dtype, co
  * Arguments that the calls share:
  * logits        device [rows][vocab], MIL_F32 or MIL_BF16, aligned to its element; row r
  *               starts row_stride elements after row r - 1 (row_stride >= vocab, so a
- *               padded vocabulary needs no copy).  A logit of -inf is a masked token.
+ *               padded vocabulary needs no copy; rows * row_stride <= 2^56).  A logit of -inf
+ *               is a masked token.
  * rows          >= 0 (0: nothing is done); rows * (2 + a row's bytes / 65536) < 2^24.
  * vocab         1 .. MIL_VOCAB_MAX.
  * temperature   MIL_TEMPERATURE_MIN .. MIL_TEMPERATURE_MAX.

@@ -604,11 +604,13 @@ int mil_ssm_scan_backward(const mil_ssm_dims *d, int32_t T, int32_t dtype, const
     return debug_after("mil_ssm_scan_backward", st, true, stream, nullptr, 0);
 }
 
+// Rows so far apart that their addresses would not fit 64 bits
+static bool too_far(int32_t rows, int64_t stride) { return stride > ((int64_t)1 << 56) / (rows > 0 ? rows : 1); }
 // Checks that the calls over rows of logits share.
 static int check_rows(int32_t rows, int32_t vocab, int64_t row_stride, int32_t dtype, float temperature) {
     if (rows < 0 || vocab < 1 || row_stride < vocab || check_dtype(dtype) != MIL_OK) return MIL_E_INVALID;
     if (!(temperature >= MIL_TEMPERATURE_MIN && temperature <= MIL_TEMPERATURE_MAX)) return MIL_E_INVALID;
-    return vocab_supported(rows, vocab, dtype == MIL_BF16) ? MIL_OK : MIL_E_UNSUPPORTED;
+    return vocab_supported(rows, vocab, dtype == MIL_BF16) && !too_far(rows, row_stride) ? MIL_OK : MIL_E_UNSUPPORTED;
 }
 
 size_t mil_ssm_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t logits_dtype, int32_t top_k) {
@@ -665,6 +667,7 @@ static int check_distill(const void *logits, int32_t rows, int32_t vocab, int64_
 static int check_distill_out(const void *logits, int32_t rows, int32_t vocab, int64_t row_stride, int32_t dtype,
                              const float *grad_loss, const void *dlogits, int64_t out_stride) {
     if (out_stride < vocab) return MIL_E_INVALID;
+    if (too_far(rows, out_stride)) return MIL_E_UNSUPPORTED;
     if (rows == 0) return MIL_OK;
     if (!grad_loss || !dlogits) return MIL_E_INVALID;
     const int eb = elt_bytes(dtype);

@@ -31,3 +31,10 @@ def test_gradient_between_the_rows_of_the_logits(dt):
     for at in (3 * 256 + 100, -3 * 300 - 100):  # apart as a whole
         assert place(at, 300, dt=dt) == L.MIL_E_WORKSPACE, at
     assert place(50, 100, V=100, stride=100) == L.MIL_E_INVALID
+
+
+def test_rows_too_far_apart_are_refused():
+    """addresses that would not fit 64 bits; their arithmetic overflowed in the check of the places"""
+    assert place(128, 256, stride=1 << 55) == L.MIL_E_UNSUPPORTED
+    assert place(1 << 20, 1 << 55) == L.MIL_E_UNSUPPORTED
+    assert place(1 << 20, 256, stride=1 << 54, rows=1) == L.MIL_E_WORKSPACE
