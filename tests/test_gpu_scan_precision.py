@@ -2,11 +2,14 @@
 from the 64-bit recurrence as a whole."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
+import scan_chunk_ref
+import scan_ref
 from speculative_decode_amd import _lib as L
-from test_gpu_scan import BF, F32, check, make
+from test_gpu_scan import BF, F32, check, f64, make, step
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +31,37 @@ def test_a_large_last_token(dt_, P, N, T):
     v, dy, dh = make(dt_, 2, T, 4, P, N, 2, seed=T, carry=True, slow=True)
     v["x"][:, -1] *= 2.0 ** 27
     check(v, dy, dh)
+
+
+SLOW = [(1, 200, 16, 64, 64, 2), (2, 150, 8, 128, 128, 2), (1, 150, 8, 64, 256, 1)]
+
+
+@pytest.mark.parametrize("shape", SLOW)
+def test_states_and_dA_are_those_of_32_bits(shape):
+    """bf16 tokens, long memories: the last state, dh0 and dA, each as a whole, are no further from the
+    64-bit recurrence than twice what the recurrence in fp32 is, which rounds a state three times a
+    token (the kernel: a few times a chunk).  Operands in two bf16 parts instead of three would be
+    past it (test_scan_chunk_ref.py)."""
+    v, dy, dh = make(BF, *shape, seed=3, carry=True, slow=True)
+    got = step(v, dy, dh)
+    a = {k: f64(t) for k, t in v.items()}
+    want = scan_ref.scan(**a, dy=f64(dy), dhT=f64(dh))
+    plain = scan_chunk_ref.in_32_bits(**a, dy=f64(dy), dhT=f64(dh))
+    for k in ("h", "dh0", "dA"):
+        err, bound = np.linalg.norm(f64(got[k]) - want[k]), 2 * np.linalg.norm(plain[k] - want[k])
+        assert err <= bound, (k, err / bound)
+
+
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("shape", SLOW + [(2, 70, 8, 32, 32, 1)])
+def test_outputs_in_bf16_are_rounded_twice_at_most(shape, slow):
+    """bf16 tokens: y and dx as a whole.  A term (state entry or pair weight, times a token) is rounded to bf16
+    on its way, and the sum of independent terms so rounded is off as much as if it were rounded
+    itself: with the output's own rounding, sqrt 2 of that one.  6 % of room."""
+    v, dy, dh = make(BF, *shape, seed=13, carry=True, slow=slow)
+    got = step(v, dy, dh)
+    want = scan_ref.scan(**{k: f64(t) for k, t in v.items()}, dy=f64(dy), dhT=f64(dh))
+    for k in ("y", "dx"):
+        once = f64(torch.tensor(want[k]).to(BF))
+        err, one = np.linalg.norm(f64(got[k]) - want[k]), np.linalg.norm(once - want[k])
+        assert err <= 1.5 * one, (k, err / one)
