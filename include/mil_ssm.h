@@ -369,8 +369,8 @@ int mil_ssm_project(const mil_ssm_dims *dims, int32_t T, int32_t d_model, const 
  *               16-byte aligned, dt and ddt to their element.  A, D, the states and their gradients
  *               are fp32.  Products of bf16 tokens run in bf16 with fp32 sums; operands formed
  *               on the way are split into bf16 parts that keep all their bits wherever a
- *               state or an fp32 gradient depends on them, and rounded where only a
- *               bf16 output does.
+ *               state or an fp32 gradient depends on them, and 16 bits where only a bf16
+ *               output does.
  * lengths       device int32 [batch] or NULL (all T): tokens behind lengths[b] (cut to
  *               0..T) do not exist: they are not read, the state passes them unchanged, and
  *               their rows of y, dx, dB, dC and ddt are set to 0.

@@ -19,8 +19,9 @@
 //
 // The state is kept as result tiles with lanes along n and registers along p, a wave owning
 // whole columns of n: the operand that contracts p, for dB, dC and the scalar products, with
-// nothing summed across waves.  What contracts n (y and dx) reads a copy of the state's
-// leading bf16 part, made in LDS once per chunk, transposed.
+// nothing summed across waves.  What contracts n (y and dx) reads copies of the state's two
+// leading bf16 parts, made in LDS once per chunk, transposed (for dx, where LDS has room for
+// one, the second part first and the first in its place).
 //
 // The columns of p are independent of each other but for sums (dB, dC, ddt, dA), so a head
 // whose state is larger than 16384 values is walked as two or more heads of fewer columns: a
@@ -30,10 +31,11 @@
 // Rounding: token operands are exact.  The state, its gradient and weighted tokens are
 // split into three bf16 parts (all 24 bits) wherever a state or the gradient of a decay
 // depends on them: an entry of dA is a long sum of terms of either sign, and two parts left
-// it 1e-6 to 4e-6 off.  The pair weights behind dB and dC are split in two, and their rows per head are
-// kept to 24 bits until the group's are summed (rounded to bf16 there, the sum was off by
-// 1.4 to 1.6 times its own rounding); the pair weights of y and dx, and the state's part in
-// them, are rounded once, next to the rounding of the output itself.
+// it 1e-6 to 4e-6 off.  What only outputs in bf16 depend on is split in two parts (16 bits): the pair
+// weights, and the states in y and dx.  (In one part the walks were 8 and 10 % faster, but y and
+// dx after a few tokens from a given state 1.4 times as far off as their own rounding.)  dB and dC per
+// head are kept to the upper 24 bits of fp32, 16 of them significant, until the group's are summed
+// (rounded to bf16 there, the sum was off by 1.4 to 1.6 times its own rounding).
 //
 // Tokens and pair weights sit in LDS row by row, pieces of 4 columns turned about per row so
 // that no read meets a bank twice; the transposed operands (inner index = row) are read with
@@ -496,9 +498,9 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
     typedef Tiles<P, N> Own;
     extern __shared__ __align__(16) char lds[];
     Scalars *sc = reinterpret_cast<Scalars *>(lds);
-    const Rows<kQ> M{reinterpret_cast<bf16 *>(sc + 2)};  // pair weights: row t, column s
-    const Rows<N> B{M.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
-    const Rows<P> X{C.p + Rows<N>::ELEMS}, Hs{X.p + Rows<P>::ELEMS};  // Hs: the state's leading part, row n
+    const Rows<kQ> M{reinterpret_cast<bf16 *>(sc + 2)}, ML{M.p + Rows<kQ>::ELEMS};  // pair weights in two parts: row t, column s
+    const Rows<N> B{ML.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
+    const Rows<P> X{C.p + Rows<N>::ELEMS}, Hs{X.p + Rows<P>::ELEMS}, Hl{Hs.p + N * P};  // the state's two leading parts, row n
     const Walk w = walk_of(p, p.nseg, p.segc);
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4,
               c = lane & 15;
@@ -511,7 +513,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
     int co_n = Rows<N>::col_off(), co_p = Rows<P>::col_off();
     const float A = p.A[w.h], D = p.D[w.h];
     // tiles of later sources stay zero
-    for (int i = tid; i < Rows<kQ>::ELEMS / 8; i += TH) reinterpret_cast<uint4 *>(M.p)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 2 * Rows<kQ>::ELEMS / 8; i += TH) reinterpret_cast<uint4 *>(M.p)[i] = make_uint4(0, 0, 0, 0);
     barrier();
 
     f32x4 hn[NC][P / 16] = {};
@@ -545,7 +547,11 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
             if (nt * 16 >= N) continue;
 #pragma unroll
             for (int i = 0; i < P / 16; ++i) {
-                Hs.put4(ro_p, 16 * nt, 16 * i, pack2(hn[k][i][0], hn[k][i][1]), pack2(hn[k][i][2], hn[k][i][3]));
+                uint32_t h0, l0, h1, l1;
+                split2(hn[k][i][0], hn[k][i][1], h0, l0);
+                split2(hn[k][i][2], hn[k][i][3], h1, l1);
+                Hs.put4(ro_p, 16 * nt, 16 * i, h0, h1);
+                Hl.put4(ro_p, 16 * nt, 16 * i, l0, l1);
                 if constexpr (KEEP) keep[(nt * (P / 16) + i) * 64] = hn[k][i];
             }
         }
@@ -568,7 +574,11 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
                 m[r] = (st < tt || 4 * q + r <= c)
                            ? S[r] * __builtin_amdgcn_exp2f((ht - hs[r]) + (lt - ls[r])) * ds[r]
                            : 0.f;
-            M.put4(ro_q, 16 * tt, 16 * st, pack2(m[0], m[1]), pack2(m[2], m[3]));
+            uint32_t h0, l0, h1, l1;
+            split2(m[0], m[1], h0, l0);
+            split2(m[2], m[3], h1, l1);
+            M.put4(ro_q, 16 * tt, 16 * st, h0, h1);
+            ML.put4(ro_q, 16 * tt, 16 * st, l0, l1);
         }
         barrier();
         if (ch + 1 < w.c1) fetch(ch + 1);
@@ -582,9 +592,13 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
                 f32x4 a[Own::TT] = {};
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
-                    const bf16x8 h = Hs.col(co_p, p0, k);
+                    const bf16x8 h = Hs.col(co_p, p0, k), l = Hl.col(co_p, p0, k);
 #pragma unroll
-                    for (int t = 0; t < Own::TT; ++t) a[t] = mfma(h, C.row(ro_n, 16 * (t0 + t), k), a[t]);
+                    for (int t = 0; t < Own::TT; ++t) {
+                        const bf16x8 ct = C.row(ro_n, 16 * (t0 + t), k);
+                        a[t] = mfma(l, ct, a[t]);
+                        a[t] = mfma(h, ct, a[t]);
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < Own::TT; ++t) a[t] *= s.up[16 * (t0 + t) + c];
@@ -593,7 +607,10 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
                     const bf16x8 xt = X.col(co_p, p0, i);
 #pragma unroll
                     for (int t = 0; t < Own::TT; ++t)
-                        if (t0 + t >= 2 * i) a[t] = mfma(xt, M.row(ro_q, 16 * (t0 + t), i), a[t]);
+                        if (t0 + t >= 2 * i) {
+                            a[t] = mfma(xt, ML.row(ro_q, 16 * (t0 + t), i), a[t]);
+                            a[t] = mfma(xt, M.row(ro_q, 16 * (t0 + t), i), a[t]);
+                        }
                 }
 #pragma unroll
                 for (int t = 0; t < Own::TT; ++t)
@@ -619,12 +636,16 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
 }
 
 // ---------------------------------------------------------------- backward
-// Scalars that a chunk's waves hand to the one that finishes the exponents' gradients
-template <int N>
+// Scalars that a chunk's waves hand to the one that finishes the exponents' gradients, next to the
+// pairs of the chunk after: from the pairs, which make the next ones then, ..
 struct Sums {
     float col[kT][kQ];      // sum over the targets of tile i of W(t, s)
     float row[kT][kQ];      // sum over the sources of tile j of dt_s W(t, s), j before t's tile
     float diag[kQ];         // pairs of u's own tile that cross u
+};
+// .. and from the states
+template <int N>
+struct Ends {
     float E[N / 16][kQ], F[N / 16][kQ];
     float dot[8];
 };
@@ -640,9 +661,11 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
     typedef Tiles<P, N> Own;
     extern __shared__ __align__(16) char lds[];
     Scalars *sc = reinterpret_cast<Scalars *>(lds);
-    Sums<N> *sums = reinterpret_cast<Sums<N> *>(sc + 2);  // [2]
-    // pair weights, row s, column t: of dx (rounded once), and of dB and dC in two parts
-    const Rows<kQ> M{reinterpret_cast<bf16 *>(sums + 2)}, DH{M.p + Rows<kQ>::ELEMS}, DL{DH.p + Rows<kQ>::ELEMS};
+    Sums *sums = reinterpret_cast<Sums *>(sc + 2);  // [2]
+    Ends<N> &ends = *reinterpret_cast<Ends<N> *>(sums + 2);
+    // pair weights, row s, column t: of dx, and of dB and dC, in two parts each
+    const Rows<kQ> M{reinterpret_cast<bf16 *>(&ends + 1)}, ML{M.p + Rows<kQ>::ELEMS}, DH{ML.p + Rows<kQ>::ELEMS},
+        DL{DH.p + Rows<kQ>::ELEMS};
     const Rows<N> B{DL.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
     const Rows<P> X{C.p + Rows<N>::ELEMS}, Y{X.p + Rows<P>::ELEMS}, Ls{Y.p + Rows<P>::ELEMS};
     const Walk w = walk_of(p, p.nseg, p.segc);
@@ -659,7 +682,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
     int co_n = Rows<N>::col_off(), co_p = Rows<P>::col_off(), co_q = Rows<kQ>::col_off();
     const float A = p.A[w.h], D = p.D[w.h];
     // tiles of earlier targets stay zero
-    for (int i = tid; i < 3 * Rows<kQ>::ELEMS / 8; i += TH)
+    for (int i = tid; i < 4 * Rows<kQ>::ELEMS / 8; i += TH)
         reinterpret_cast<uint4 *>(M.p)[i] = make_uint4(0, 0, 0, 0);
     barrier();
 
@@ -678,15 +701,15 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
     double dA = 0.0, dD = 0.0;
     // du, decay: the chunk's dt of this lane's token and its whole decay
     auto finish = [&](int ch, float du, float decay) {
-        const Sums<N> &sm = sums[ch & 1];
+        const Sums &sm = sums[ch & 1];
         const int have = min(kQ, p.T - ch * kQ);
         // gradient of each token's exponent; lane u, m = its tile
         const int u = lane, m = lane >> 4;
         float e = 0.f, f = 0.f, all = 0.f;
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) e += sm.E[i][u], f += sm.F[i][u];
+        for (int i = 0; i < N / 16; ++i) e += ends.E[i][u], f += ends.F[i][u];
 #pragma unroll
-        for (int i = 0; i < NW; ++i) all += sm.dot[i];
+        for (int i = 0; i < NW; ++i) all += ends.dot[i];
         const float own = sm.col[m][u];
         float after = 0.f;  // targets in later tiles
         for (int i = m + 1; i < kT; ++i) after += sm.col[i][u];
@@ -735,19 +758,27 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         asm volatile("" : "+v"(ro_n), "+v"(ro_p), "+v"(ro_q), "+v"(co_n), "+v"(co_p), "+v"(co_q), "+v"(lane));
         q = lane >> 4, c = lane & 15;
         const Scalars &s = sc[ch & 1];
-        Sums<N> &sm = sums[ch & 1];
+        Sums &sm = sums[ch & 1];
         lB.store(B);
         lC.store(C);
         lX.store(X);
         lY.store(Y);
+        // the state's second part, and the first when that has been used
+        auto put_part = [&](bool second) {
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int nt = wave + k * NW;
-            if (nt * 16 >= N) continue;
+            for (int k = 0; k < NC; ++k) {
+                const int nt = wave + k * NW;
+                if (nt * 16 >= N) continue;
 #pragma unroll
-            for (int i = 0; i < P / 16; ++i)
-                Ls.put4(ro_p, 16 * nt, 16 * i, pack2(ln[k][i][0], ln[k][i][1]), pack2(ln[k][i][2], ln[k][i][3]));
-        }
+                for (int i = 0; i < P / 16; ++i) {
+                    uint32_t h0, l0, h1, l1;
+                    split2(ln[k][i][0], ln[k][i][1], h0, l0);
+                    split2(ln[k][i][2], ln[k][i][3], h1, l1);
+                    Ls.put4(ro_p, 16 * nt, 16 * i, second ? l0 : h0, second ? l1 : h1);
+                }
+            }
+        };
+        put_part(true);
         barrier();
         f32x4 kept[NC][P / 16];
         {
@@ -804,9 +835,12 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
                 v[r] = W * ds;
             }
             uint32_t h0, l0, h1, l1;
+            split2(m[0], m[1], h0, l0);
+            split2(m[2], m[3], h1, l1);
+            M.put4(ro_q, 16 * st, 16 * tt, h0, h1);
+            ML.put4(ro_q, 16 * st, 16 * tt, l0, l1);
             split2(d[0], d[1], h0, l0);
             split2(d[2], d[3], h1, l1);
-            M.put4(ro_q, 16 * st, 16 * tt, pack2(m[0], m[1]), pack2(m[2], m[3]));
             DH.put4(ro_q, 16 * st, 16 * tt, h0, h1);
             DL.put4(ro_q, 16 * st, 16 * tt, l0, l1);
             col = sum_q(col);
@@ -829,23 +863,35 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
                 }
             }
         }
+        // the states' part of dx, 16 columns of p, lanes along s
+        f32x4 ax[Own::PT][Own::TT] = {};
+        auto states_of_dx = [&]() {
+#pragma unroll
+            for (int u = 0; u < Own::PT; ++u)
+#pragma unroll 4
+                for (int k = 0; k < N / 32; ++k) {
+                    const bf16x8 l = Ls.col(co_p, Own::p0(wave, u), k);
+#pragma unroll
+                    for (int t = 0; t < Own::TT; ++t)
+                        ax[u][t] = mfma(l, B.row(ro_n, 16 * (Own::t0(wave) + t), k), ax[u][t]);
+                }
+        };
+        phase();
+        states_of_dx();
         barrier();
+        put_part(false);
         if (wave == NW - 1 && ch - 2 >= w.c0) dt = load_dt(p, w, ch - 2);
         last_dt = s.dt[lane], last_decay = s.up[kQ - 1];
         const int have = min(kQ, p.T - ch * kQ);
+        barrier();
         auto make_dx = [&]() {
             const Buf out = view(oX + (int64_t)ch * kQ * sp, (int64_t)have * sp);
             const int t0 = Own::t0(wave);
+            states_of_dx();
 #pragma unroll
-            for (int u = 0; u < Own::PT; ++u) {  // dx: 16 columns of p, lanes along s
+            for (int u = 0; u < Own::PT; ++u) {
                 const int p0 = Own::p0(wave, u);
-                f32x4 a[Own::TT] = {};
-#pragma unroll 4
-                for (int k = 0; k < N / 32; ++k) {
-                    const bf16x8 l = Ls.col(co_p, p0, k);
-#pragma unroll
-                    for (int t = 0; t < Own::TT; ++t) a[t] = mfma(l, B.row(ro_n, 16 * (t0 + t), k), a[t]);
-                }
+                f32x4(&a)[Own::TT] = ax[u];
 #pragma unroll
                 for (int t = 0; t < Own::TT; ++t) a[t] *= s.down[16 * (t0 + t) + c] * s.dt[16 * (t0 + t) + c];
 #pragma unroll
@@ -853,7 +899,10 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
                     const bf16x8 yt = Y.col(co_p, p0, i);
 #pragma unroll
                     for (int t = 0; t < Own::TT; ++t)
-                        if (t0 + t < 2 * i + 2) a[t] = mfma(yt, M.row(ro_q, 16 * (t0 + t), i), a[t]);
+                        if (t0 + t < 2 * i + 2) {
+                            a[t] = mfma(yt, ML.row(ro_q, 16 * (t0 + t), i), a[t]);
+                            a[t] = mfma(yt, M.row(ro_q, 16 * (t0 + t), i), a[t]);
+                        }
                 }
                 float dd = 0.f;
 #pragma unroll
@@ -899,7 +948,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
                     a[t] *= s.down[16 * t + c];
                     const f32x4 b = B.four(ro_n, 16 * t, n0);
                     const float f = sum_q((a[t][0] * b[0] + a[t][1] * b[1]) + (a[t][2] * b[2] + a[t][3] * b[3]));
-                    if (q == 0) sm.F[nt][16 * t + c] = f;
+                    if (q == 0) ends.F[nt][16 * t + c] = f;
                     a[t] *= s.dt[16 * t + c];
                 }
 #pragma unroll
@@ -927,7 +976,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
                     a[t] *= s.up[16 * t + c];
                     const f32x4 b = C.four(ro_n, 16 * t, n0);
                     const float e = sum_q((a[t][0] * b[0] + a[t][1] * b[1]) + (a[t][2] * b[2] + a[t][3] * b[3]));
-                    if (q == 0) sm.E[nt][16 * t + c] = e;
+                    if (q == 0) ends.E[nt][16 * t + c] = e;
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -950,7 +999,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         }
 #pragma unroll
         for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-        if (lane == 0) sm.dot[wave] = dot;
+        if (lane == 0) ends.dot[wave] = dot;
         phase();
         f32x4 wt[4];
         token_weights(s.up, wt);
@@ -1034,12 +1083,12 @@ constexpr size_t lds_segments() {
 }
 template <int P, int N>
 constexpr size_t lds_forward() {
-    return 2 * sizeof(Scalars) + (Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + Rows<P>::ELEMS + N * P) * 2;
+    return 2 * sizeof(Scalars) + (2 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + Rows<P>::ELEMS + 2 * N * P) * 2;
 }
 template <int P, int N>
 constexpr size_t lds_backward() {
-    return 2 * sizeof(Scalars) + 2 * sizeof(Sums<N>) +
-           (3 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + 2 * Rows<P>::ELEMS + N * P) * 2;
+    return 2 * sizeof(Scalars) + 2 * sizeof(Sums) + sizeof(Ends<N>) +
+           (4 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + 2 * Rows<P>::ELEMS + N * P) * 2;
 }
 unsigned sub_grid(const ScanParams &p) { return (unsigned)(p.nseq * p.H * p.parts * p.nsub); }
 unsigned fold_grid(const ScanParams &p) {
@@ -1067,7 +1116,7 @@ hipError_t launch(unsigned grid, unsigned threads, size_t lds, hipStream_t s, co
 
 template <int P, int N>
 hipError_t forward(const ScanParams &p, bool keep, hipStream_t s) {
-    static_assert(lds_backward<P, N>() <= 160 * 1024, "LDS of a compute unit");
+    static_assert(lds_backward<P, N>() <= 160 * 1024 && lds_forward<P, N>() <= 160 * 1024, "LDS of a compute unit");
     const unsigned grid = (unsigned)(p.nseq * p.H * p.parts * p.nseg), th = waves<N>() * 64;
     hipError_t e = hipSuccess;
     if (p.nseg > 1) {

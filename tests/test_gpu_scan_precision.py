@@ -53,15 +53,16 @@ def test_states_and_dA_are_those_of_32_bits(shape):
 
 
 @pytest.mark.parametrize("slow", [False, True])
-@pytest.mark.parametrize("shape", SLOW + [(2, 70, 8, 32, 32, 1)])
-def test_outputs_in_bf16_are_rounded_twice_at_most(shape, slow):
-    """bf16 tokens: y and dx as a whole.  A term (state entry or pair weight, times a token) is rounded to bf16
-    on its way, and the sum of independent terms so rounded is off as much as if it were rounded
-    itself: with the output's own rounding, sqrt 2 of that one.  6 % of room."""
+@pytest.mark.parametrize("shape", SLOW + [(2, 70, 8, 32, 32, 1), (3, 20, 8, 128, 128, 2), (4, 1, 8, 32, 64, 1)])
+def test_y_and_dx_are_rounded_once(shape, slow):
+    """bf16 tokens: y and dx, each as a whole, are as far from the exact values as those rounded to bf16 are.
+    What is rounded on the way keeps 16 bits and more (2^-17 of a term at most, against 2^-9 for the
+    output), so 5 % of room is plenty; a term rounded to bf16 would take sqrt 2 where the states outweigh the
+    tokens, as after a few tokens from a given state."""
     v, dy, dh = make(BF, *shape, seed=13, carry=True, slow=slow)
     got = step(v, dy, dh)
     want = scan_ref.scan(**{k: f64(t) for k, t in v.items()}, dy=f64(dy), dhT=f64(dh))
     for k in ("y", "dx"):
         once = f64(torch.tensor(want[k]).to(BF))
         err, one = np.linalg.norm(f64(got[k]) - want[k]), np.linalg.norm(once - want[k])
-        assert err <= 1.5 * one, (k, err / one)
+        assert err <= 1.05 * one, (k, err / one)
