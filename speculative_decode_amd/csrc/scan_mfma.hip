@@ -359,8 +359,8 @@ __device__ __forceinline__ void token_weights(const float *a, f32x4 (&w)[4]) {
 // ---------------------------------------------------------------- segments
 // The own contribution to the state (BACK: to its gradient), [N][P], and the whole exponent
 // of each sub-segment (a segment, or a half: this launch is light enough for two workgroups
-// on a compute unit).  8192 tokens, 32 heads of 128 x 128: 40 us, 79 MB read at 2.0 TB/s; LDS
-// (50 %) and vector ALU (47 %) take turns with the matrix cores (35 %).
+// on a compute unit).  8192 tokens, 32 heads of 128 x 128: 41 us, 79 MB read at 1.9 TB/s; LDS
+// (51 %) and vector ALU (48 %) take turns with the matrix cores (36 %).
 template <int P, int N, bool BACK>
 __global__ __launch_bounds__(waves<N>() * 64) void scan_segments(const ScanParams p) {
     constexpr int NW = waves<N>(), TH = NW * 64, NC = (N / 16 + NW - 1) / NW;
@@ -488,10 +488,11 @@ struct Tiles {
 // ---------------------------------------------------------------- forward
 // KEEP: leave the state entering each chunk behind for the backward walk, as the tiles it is held
 // in: [n tile][p tile][lane][4].
-// 8192 tokens, 32 heads of 128 x 128 (60 GFLOP with its backward call): 97 us, 109 with the
-// states left behind (456 MB at 4.2 TB/s; unit by unit LDS 44 %, vector ALU 38 %, matrix cores
-// 19 % busy).  What bounds it is that a chunk's phases follow one another: with 137 KB of LDS
-// and the state in registers one workgroup of two waves a SIMD has the compute unit.
+// 8192 tokens, 32 heads of 128 x 128 (60 GFLOP with its backward call): 112 us, 123 with the
+// states left behind (456 MB at 3.7 TB/s; unit by unit LDS 50 %, vector ALU 43 %, matrix cores
+// 22 % busy).  What bounds it is that a chunk's phases follow one another: with 131 KB of LDS one
+// workgroup of two waves a SIMD has the compute unit.  (Narrower walks, two of which fit, would
+// read B and C and form the pairs once more each; not measured.)
 template <int P, int N, bool KEEP>
 __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p) {
     constexpr int NW = waves<N>(), TH = NW * 64, NC = (N / 16 + NW - 1) / NW;
@@ -650,11 +651,12 @@ struct Ends {
     float dot[8];
 };
 
-// 8192 tokens, 32 heads of 128 x 128: 239 us, 723 MB at 3.0 TB/s; LDS 51 %, vector ALU 48 %
-// and matrix cores 23 % busy, as in the walk forward one after another; 27000 cycles a chunk, of
-// which the matrix products alone need 6600.  4 sequences of up to 2001 tokens, 32 heads of
-// 128 x 256 in two parts each: 574 us.  (With operands in two parts 11 us less, but dA 1e-6 off
-// and more.)
+// 8192 tokens, 32 heads of 128 x 128: 265 us, 723 MB at 2.7 TB/s; LDS 52 %, vector ALU 50 %
+// and matrix cores 23 % busy, as in the walk forward one after another; 31700 cycles a chunk, of
+// which the matrix products alone need 7200.  4 sequences of up to 2001 tokens, 32 heads of
+// 128 x 256 in two parts each: 597 us, 1.57 GB at 2.6 TB/s (chunks behind a sequence's end are walked
+// like any other, on zeros).  (Two parts instead of three behind the states and dA took 11 us less
+// at an earlier stage, but left dA 1e-6 off and more.)
 template <int P, int N>
 __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanParams p) {
     constexpr int NW = waves<N>(), TH = NW * 64, NC = (N / 16 + NW - 1) / NW;
@@ -1138,9 +1140,9 @@ hipError_t backward(const ScanParams &p, hipStream_t s) {
     if (e == hipSuccess) e = launch<scan_walk_back<P, N>>(grid, th, lds_backward<P, N>(), s, p);
     return e;
 }
-// Columns of p that a walk takes: all of them up to 128 and to a state of 16384 values.  (At
-// 128 x 256 whole heads spilled registers: walk back 1345 us, in two parts 936, at 4 sequences of
-// up to 2001 tokens and 32 heads and an early stage of both.)
+// Columns of p that a walk takes: all of them up to 128 and to a state of 16384 values.  (Whole heads
+// of 128 x 256 would need 207 KB of LDS.  An early form that fitted spilled registers: walk back
+// 1345 us, in two parts 936, at 4 sequences of up to 2001 tokens and 32 heads.)
 int columns(int P, int N) {
     int c = P < 128 ? P : 128;
     while (c * N > 16384) c /= 2;
@@ -1167,17 +1169,18 @@ hipError_t by_shape(int P, int N, F f) {
 
 }  // namespace
 
-// Against the general kernels, bf16, 32 heads of 128 x 128, forward and backward: 1024 tokens 105 us
-// against 966, 8192 tokens 500 against 6747.  (P or N of 16 would leave half of every operand's
-// inner indices empty.)
+// Against the general kernels, bf16, 32 heads of 128 x 128, all kernels of forward and backward:
+// 1024 tokens 113 us against 390, 8192 tokens 545 against 3190.  (P or N of 16 would leave half of
+// every operand's inner indices empty.)
 bool scan_mfma_supported(const ScanParams &p) {
     // (the last: a chunk's rows, of up to 4 parts of a head, stay within the 2 GiB of a bounded view)
     return p.bf && p.P >= 32 && p.N >= 32 && (int64_t)p.H * (p.P > 4 * p.N ? p.P : 4 * p.N) < 1 << 23;
 }
 // Segments: as many as fill the chip with one workgroup per compute unit, but none shorter
 // than two chunks (the launch that prepares them walks every segment but one).  8192 tokens, 32
-// heads of 128 x 128, at an early stage: walk back 1895 us in one segment, 969 in two, 510 in four,
-// 290 in eight; walk forward 875, 454, 250, 124; the preparing launch 150, 80, 48 each way.
+// heads of 128 x 128: walk back 1602 us in one segment, 810 in two, 422 in four, 266 in eight; walk
+// forward 701, 353, 189, 123; the preparing launch 71 us in two segments, 41 in four and in eight,
+// with its fold 76, 48 and 53 each way.
 void scan_mfma_cut(ScanParams &p) {
     p.nch = (p.T + kQ - 1) / kQ;
     p.parts = p.P / columns(p.P, p.N);
@@ -1188,7 +1191,8 @@ void scan_mfma_cut(ScanParams &p) {
     p.segc = (p.nch + n - 1) / n;
     p.nseg = (p.nch + p.segc - 1) / p.segc;
     // halves where they are long enough to be worth the larger fold (8 chunks and more: 8192
-    // tokens of 32 heads 47 -> 39 us against 8 -> 11 us; at 2 chunks the fold loses more)
+    // tokens of 32 heads 46 -> 41 us against 8.5 -> 12 us; at 2 chunks, 1024 tokens, 11.7 -> 13.3
+    // and 8.3 -> 11.4)
     p.subc = p.segc % 2 == 0 && p.segc >= 8 ? p.segc / 2 : p.segc;
     p.nsub = (p.nch + p.subc - 1) / p.subc;
 }

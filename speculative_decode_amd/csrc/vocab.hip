@@ -6,7 +6,9 @@
 // is formed from the row's maximum m and sums of e_i = e^{(z_i - m)/T}:
 //   log q_i = (z_i - m)/T - log S,                  S = sum e_i
 //   entropy = log S + (sum e_i (m - z_i)/T) / S     (a sum of terms >= 0: nothing cancels)
-// All sums are fp32 per thread (at most 128 terms) and wider beyond the workgroup.
+// Sums are fp32 over a thread's terms (at most 136) and a tree over the workgroup's threads; what a
+// row's slices or waves leave is added up in fp32 for the log probabilities (at most 33 slices)
+// and in fp64 for the loss.
 //
 // What bounds them: each logit has to be read once (2 or 4 bytes) and costs one exponential
 // and about ten vector operations, which at 2 bytes is close to the time of the read, so
@@ -194,8 +196,8 @@ struct LogprobParams {
 // holds a NaN, the exact k-th key is found by bisection over its 32 bits first, and elements
 // equal to it are taken in rising id order as far as they are needed; so are masked ones.
 //
-// 4096 rows of 128256 bf16 values, 64 alternatives: 260 us with the joining launch, 1.05 GB at
-// 4.0 TB/s, vector ALU 93 % busy.  128 rows, 20 alternatives: 20 us (1.7 TB/s), one round of
+// 4096 rows of 128256 bf16 values, 64 alternatives: 276 us with the joining launch, 1.05 GB at
+// 3.8 TB/s, vector ALU 94 % busy.  128 rows, 20 alternatives: 20 us (1.7 TB/s), one round of
 // workgroups: the chain of load, maximum, sums and selection.  One row: 13 us.
 template <bool BF, int VPT>
 __global__ __launch_bounds__(kNT, 4) void logprob_slice(const LogprobParams p) {
@@ -620,8 +622,8 @@ __device__ __forceinline__ float sum_vec(u32x4 raw, float m, const Scale &c) {
     return sum;
 }
 
-// Sums of a slice.  515 rows of 32003 fp32 values: 21 us (66 MB at 3.1 TB/s), the gradient's launch
-// below 27 (133 MB at 4.9 TB/s).
+// Sums of a slice.  515 rows of 32003 fp32 values: 24 us (67 MB at 2.8 TB/s), the gradient's launch
+// below 23 (133 MB at 5.8 TB/s).
 template <bool BF, int VPT>
 __global__ __launch_bounds__(kNT, 4) void distill_slice(const DistillParams p) {
     constexpr int EPV = Vec<BF>::EPV;
@@ -667,7 +669,7 @@ __global__ __launch_bounds__(kNT, 4) void distill_slice(const DistillParams p) {
     if (tid == 0) p.part[item] = make_float4(m, (sSum[0] + sSum[1]) + (sSum[2] + sSum[3]), 0.f, 0.f);
 }
 
-// Loss of a row from its slices: one wave per row.  6 us for 515 rows.
+// Loss of a row from its slices: one wave per row.  7 us for 515 rows.
 template <bool BF>
 __global__ __launch_bounds__(kNT) void distill_join(const DistillParams p) {
     const int lane = threadIdx.x & 63;
@@ -788,8 +790,10 @@ __global__ __launch_bounds__(kNT, 4) void distill_grad(const DistillParams p) {
 // the next: a vector's registers are free once its gradient is formed.  The last wave holds no
 // logits: it prepares the teacher's side of the next row and works out the loss of this one,
 // in double precision, while the others are busy with the gradient.  Rows start and end on
-// 16-byte boundaries.  4096 rows of 128256 bf16 values with 64 alternatives: 489 us, 2.12 GB at 4.3
-// TB/s, 0.91 of the rate of a large copy, which bounds it (vector ALU 62 % busy).
+// 16-byte boundaries.  4096 rows of 128256 bf16 values with 64 alternatives: 492 us, 2.12 GB at 4.3
+// TB/s, 0.70 of the rate of an elementwise pass over as much (vector ALU 59 % busy): a row's
+// maximum, sums and gradient follow one another, and only the gradient's part of them stores, and
+// loads the next row.
 struct RowTeacher {
     int id[64];
     float p[64], z[64];
@@ -950,8 +954,8 @@ MIL_BY_SIZE(distill_slice)
 MIL_BY_SIZE(distill_grad)
 
 // Rows that one workgroup holds whole (distill_rows): up to what fits, in vectors.  Against the
-// three launches of the separate calls (loss with gradient, bf16, us): 4096 rows of 128256 477 :
-// 616, of 32000 126 : 190, of 8192 60 : 80; 128 rows of 32000 15 : 21.  Short rows in large
+// three launches of the separate calls (loss with gradient, bf16, us): 4096 rows of 128256 492 :
+// 635, of 32000 151 : 209, of 8192 54 : 75; 128 rows of 32000 15 : 21.  Short rows in large
 // numbers wait for one another (4096 rows of 1000 60 : 48, 2048 rows 33 : 29, 1024 rows 22 : 23).
 // A few rows of 128256 are the one place where the slices' more workgroups are ahead (4 rows
 // 25 : 21), not far enough for a rule of its own.
@@ -973,9 +977,9 @@ hipError_t run_distill_rows(bool bf, int nv, const DistillParams &p, hipStream_t
     const std::integral_constant<int, 8> w8;
     const std::integral_constant<int, 16> w16;
     // Eight waves, and two or three workgroups on a compute unit, as far as they hold a row (16384
-    // bf16 values, 4096 rows: 73 us, with one workgroup of 16 waves 96); the vectors a thread in
-    // steps, since those without a value still cost their share of the work (32000 values: 9
-    // vectors 126 us, 8 in twice the waves 214)
+    // bf16 values, 4096 rows: 69 us, with one workgroup of 16 waves 182); the vectors a thread in
+    // steps, since those without a value still cost their share of the work (32000 values, 64
+    // alternatives: 9 vectors 151 us, as many in twice the waves 266)
     const int each = (nv + 7 * 64 - 1) / (7 * 64);
     if (each <= 3)
         go(w8, std::integral_constant<int, 3>{});
