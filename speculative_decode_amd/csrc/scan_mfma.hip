@@ -20,8 +20,8 @@
 // The state is kept as result tiles with lanes along n and registers along p, a wave owning
 // whole columns of n: the operand that contracts p, for dB, dC and the scalar products, with
 // nothing summed across waves.  What contracts n (y and dx) reads copies of the state's two
-// leading bf16 parts, made in LDS once per chunk, transposed (for dx, where LDS has room for
-// one, the second part first and the first in its place).
+// leading bf16 parts, made in LDS once per chunk, transposed (where LDS has room for one, the
+// second part first and then the first in its place).
 //
 // The columns of p are independent of each other but for sums (dB, dC, ddt, dA), so a head
 // whose state is larger than 16384 values is walked as two or more heads of fewer columns: a
@@ -485,6 +485,41 @@ struct Tiles {
     static __device__ __forceinline__ int t0(int wave) { return TT < kT ? wave / (P / 16) * TT : 0; }
 };
 
+// The first or second bf16 part of a state held as result tiles, as rows n for what contracts n
+template <int P, int N, int NC>
+__device__ __forceinline__ void put_part(const Rows<P> &to, int o, int wave, bool second, const f32x4 (&h)[NC][P / 16]) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        const int nt = wave + k * waves<N>();
+        if (nt * 16 >= N) continue;
+#pragma unroll
+        for (int i = 0; i < P / 16; ++i) {
+            uint32_t h0, l0, h1, l1;
+            split2(h[k][i][0], h[k][i][1], h0, l0);
+            split2(h[k][i][2], h[k][i][3], h1, l1);
+            to.put4(o, 16 * nt, 16 * i, second ? l0 : h0, second ? l1 : h1);
+        }
+    }
+}
+// a += (columns of p of a part, or of two) x (rows of tokens), for the wave's own tiles
+template <int P, int N, bool TWO>
+__device__ __forceinline__ void times_state(const Rows<P> &h, const Rows<P> &low, const Rows<N> &rows, int ho, int o,
+                                            int wave, f32x4 (&a)[Tiles<P, N>::PT][Tiles<P, N>::TT]) {
+    typedef Tiles<P, N> Own;
+#pragma unroll
+    for (int u = 0; u < Own::PT; ++u)
+#pragma unroll 4
+        for (int k = 0; k < N / 32; ++k) {
+            const bf16x8 x = h.col(ho, Own::p0(wave, u), k), y = TWO ? low.col(ho, Own::p0(wave, u), k) : x;
+#pragma unroll
+            for (int t = 0; t < Own::TT; ++t) {
+                const bf16x8 r = rows.row(o, 16 * (Own::t0(wave) + t), k);
+                if constexpr (TWO) a[u][t] = mfma(y, r, a[u][t]);
+                a[u][t] = mfma(x, r, a[u][t]);
+            }
+        }
+}
+
 // ---------------------------------------------------------------- forward
 // KEEP: leave the state entering each chunk behind for the backward walk, as the tiles it is held
 // in: [n tile][p tile][lane][4].
@@ -493,18 +528,39 @@ struct Tiles {
 // 22 % busy).  What bounds it is that a chunk's phases follow one another: with 131 KB of LDS one
 // workgroup of two waves a SIMD has the compute unit.  (Narrower walks, two of which fit, would
 // read B and C and form the pairs once more each; not measured.)
+// The state's two parts have a place in LDS each, or take one in turn, the second first, where a compute unit
+// then has room for one workgroup more.  In turn costs a barrier a chunk and reads B and C once for each
+// part: 8192 tokens, 32 heads of 128 x 128, where nothing is won, 135 us against 123; 16 sequences of 1024 tokens,
+// 32 heads of 64 x 128, without states left behind, 131 us against 147.
+template <int P, int N>
+constexpr size_t lds_forward(int places) {
+    return 2 * sizeof(Scalars) + (2 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + Rows<P>::ELEMS + places * N * P) * 2;
+}
+// Workgroups to a compute unit: with 128 columns the registers leave room for two, with fewer for four.  (64 x 128
+// spills one or two registers a lane for its second one; with less unrolling none, but 1 to 2 % slower.)
+template <int P, int N>
+constexpr int groups(int places) {
+    const int n = (int)(160 * 1024 / lds_forward<P, N>(places)), most = P == 128 ? 2 : 4;
+    return n < most ? n : most;
+}
+template <int P, int N>
+constexpr int places() {
+    return groups<P, N>(1) > groups<P, N>(2) ? 1 : 2;
+}
 template <int P, int N, bool KEEP>
-__global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p) {
+__global__ __launch_bounds__(waves<N>() * 64, (waves<N>() / 4 * groups<P, N>(places<P, N>()))) void scan_walk(const ScanParams p) {
+    constexpr bool TURN = places<P, N>() == 1;
     constexpr int NW = waves<N>(), TH = NW * 64, NC = (N / 16 + NW - 1) / NW;
     typedef Tiles<P, N> Own;
     extern __shared__ __align__(16) char lds[];
     Scalars *sc = reinterpret_cast<Scalars *>(lds);
     const Rows<kQ> M{reinterpret_cast<bf16 *>(sc + 2)}, ML{M.p + Rows<kQ>::ELEMS};  // pair weights in two parts: row t, column s
     const Rows<N> B{ML.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
-    const Rows<P> X{C.p + Rows<N>::ELEMS}, Hs{X.p + Rows<P>::ELEMS}, Hl{Hs.p + N * P};  // the state's two leading parts, row n
+    const Rows<P> X{C.p + Rows<N>::ELEMS};
+    const Rows<P> Hs{X.p + Rows<P>::ELEMS}, Hl{TURN ? Hs.p : Hs.p + N * P};  // the state's parts, row n
     const Walk w = walk_of(p, p.nseg, p.segc);
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4,
-              c = lane & 15;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, q = lane >> 4, c = lane & 15;
     const int sn = p.G * N * 2, sp = p.H * p.P * 2;  // bytes from a token's row to the next
     const int64_t bn = w.tok0 * sn + w.g * N * 2, bp = w.tok0 * sp + (w.h * p.P + w.v * P) * 2;
     const char *gB = static_cast<const char *>(p.B) + bn, *gC = static_cast<const char *>(p.C) + bn;
@@ -535,27 +591,23 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
     }
     for (int ch = w.c0; ch < w.c1; ++ch) {
         // (see the backward walk)
-        asm volatile("" : "+v"(ro_n), "+v"(ro_p), "+v"(ro_q), "+v"(co_n), "+v"(co_p));
+        asm volatile("" : "+v"(ro_n), "+v"(ro_p), "+v"(ro_q), "+v"(co_n), "+v"(co_p), "+v"(lane));
+        q = lane >> 4, c = lane & 15;
         const Scalars &s = sc[ch & 1];
         lB.store(B);
         lC.store(C);
         lX.store(X);
         f32x4 *keep = reinterpret_cast<f32x4 *>(p.states) +
                       ((((int64_t)w.seq * p.nch + ch) * p.H + w.h) * p.parts + w.v) * (N * P / 4) + lane;
+        if constexpr (KEEP) {
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int nt = wave + k * NW;
-            if (nt * 16 >= N) continue;
+            for (int k = 0; k < NC; ++k)
 #pragma unroll
-            for (int i = 0; i < P / 16; ++i) {
-                uint32_t h0, l0, h1, l1;
-                split2(hn[k][i][0], hn[k][i][1], h0, l0);
-                split2(hn[k][i][2], hn[k][i][3], h1, l1);
-                Hs.put4(ro_p, 16 * nt, 16 * i, h0, h1);
-                Hl.put4(ro_p, 16 * nt, 16 * i, l0, l1);
-                if constexpr (KEEP) keep[(nt * (P / 16) + i) * 64] = hn[k][i];
-            }
+                for (int i = 0; i < P / 16; ++i)
+                    if ((wave + k * NW) * 16 < N) keep[((wave + k * NW) * (P / 16) + i) * 64] = hn[k][i];
         }
+        if constexpr (!TURN) put_part<P, N, NC>(Hs, ro_p, wave, false, hn);
+        put_part<P, N, NC>(Hl, ro_p, wave, true, hn);
         barrier();
         // next to the pairs, one wave forms the scalars of the next chunk
         if (wave == NW - 1 && ch + 1 < w.c1) fill_scalars(sc[(ch + 1) & 1], dt, A);
@@ -581,26 +633,25 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk(const ScanParams p)
             M.put4(ro_q, 16 * tt, 16 * st, h0, h1);
             ML.put4(ro_q, 16 * tt, 16 * st, l0, l1);
         }
+        // the state's part of y, 16 columns of p, lanes along t
+        f32x4 ay[Own::PT][Own::TT] = {};
+        if constexpr (TURN) {
+            phase();
+            times_state<P, N, false>(Hl, Hl, C, co_p, ro_n, wave, ay);
+            barrier();
+            put_part<P, N, NC>(Hs, ro_p, wave, false, hn);
+        }
         barrier();
         if (ch + 1 < w.c1) fetch(ch + 1);
         if (wave == NW - 1 && ch + 2 < w.c1) dt = load_dt(p, w, ch + 2);
         const Buf out = view(gY + (int64_t)ch * kQ * sp, (int64_t)min(kQ, p.T - ch * kQ) * sp);
         const int t0 = Own::t0(wave);
         auto make_y = [&]() {
+            times_state<P, N, !TURN>(Hs, Hl, C, co_p, ro_n, wave, ay);
 #pragma unroll
-            for (int u = 0; u < Own::PT; ++u) {  // y: 16 columns of p, lanes along t
+            for (int u = 0; u < Own::PT; ++u) {
                 const int p0 = Own::p0(wave, u);
-                f32x4 a[Own::TT] = {};
-#pragma unroll
-                for (int k = 0; k < N / 32; ++k) {
-                    const bf16x8 h = Hs.col(co_p, p0, k), l = Hl.col(co_p, p0, k);
-#pragma unroll
-                    for (int t = 0; t < Own::TT; ++t) {
-                        const bf16x8 ct = C.row(ro_n, 16 * (t0 + t), k);
-                        a[t] = mfma(l, ct, a[t]);
-                        a[t] = mfma(h, ct, a[t]);
-                    }
-                }
+                f32x4(&a)[Own::TT] = ay[u];
 #pragma unroll
                 for (int t = 0; t < Own::TT; ++t) a[t] *= s.up[16 * (t0 + t) + c];
 #pragma unroll
@@ -665,9 +716,11 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
     Scalars *sc = reinterpret_cast<Scalars *>(lds);
     Sums *sums = reinterpret_cast<Sums *>(sc + 2);  // [2]
     Ends<N> &ends = *reinterpret_cast<Ends<N> *>(sums + 2);
-    // pair weights, row s, column t: of dx, and of dB and dC, in two parts each
-    const Rows<kQ> M{reinterpret_cast<bf16 *>(&ends + 1)}, ML{M.p + Rows<kQ>::ELEMS}, DH{ML.p + Rows<kQ>::ELEMS},
-        DL{DH.p + Rows<kQ>::ELEMS};
+    // pair weights, row s, column t: of dx, and of dB and dC, in two parts each.  Of each the quarter of
+    // rows 32.. and columns ..31 is never read; the three of M, DH and DL hold the quarters that M's second
+    // part has: (rows, columns) ..31, ..31; ..31, 32..; 32.., 32..
+    const Rows<kQ> M{reinterpret_cast<bf16 *>(&ends + 1)}, DH{M.p + Rows<kQ>::ELEMS}, DL{DH.p + Rows<kQ>::ELEMS};
+    auto second = [&](int st, int half) { return half == 0 ? M : st < 2 ? DH : DL; };  // of tile row st
     const Rows<N> B{DL.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
     const Rows<P> X{C.p + Rows<N>::ELEMS}, Y{X.p + Rows<P>::ELEMS}, Ls{Y.p + Rows<P>::ELEMS};
     const Walk w = walk_of(p, p.nseg, p.segc);
@@ -684,7 +737,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
     int co_n = Rows<N>::col_off(), co_p = Rows<P>::col_off(), co_q = Rows<kQ>::col_off();
     const float A = p.A[w.h], D = p.D[w.h];
     // tiles of earlier targets stay zero
-    for (int i = tid; i < 4 * Rows<kQ>::ELEMS / 8; i += TH)
+    for (int i = tid; i < 3 * Rows<kQ>::ELEMS / 8; i += TH)
         reinterpret_cast<uint4 *>(M.p)[i] = make_uint4(0, 0, 0, 0);
     barrier();
 
@@ -765,22 +818,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         lC.store(C);
         lX.store(X);
         lY.store(Y);
-        // the state's second part, and the first when that has been used
-        auto put_part = [&](bool second) {
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                const int nt = wave + k * NW;
-                if (nt * 16 >= N) continue;
-#pragma unroll
-                for (int i = 0; i < P / 16; ++i) {
-                    uint32_t h0, l0, h1, l1;
-                    split2(ln[k][i][0], ln[k][i][1], h0, l0);
-                    split2(ln[k][i][2], ln[k][i][3], h1, l1);
-                    Ls.put4(ro_p, 16 * nt, 16 * i, second ? l0 : h0, second ? l1 : h1);
-                }
-            }
-        };
-        put_part(true);
+        put_part<P, N, NC>(Ls, ro_p, wave, true, ln);
         barrier();
         f32x4 kept[NC][P / 16];
         {
@@ -840,7 +878,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
             split2(m[0], m[1], h0, l0);
             split2(m[2], m[3], h1, l1);
             M.put4(ro_q, 16 * st, 16 * tt, h0, h1);
-            ML.put4(ro_q, 16 * st, 16 * tt, l0, l1);
+            second(st, tt >> 1).put4(ro_q, 32 + 16 * (st & 1), 16 * (tt & 1), l0, l1);
             split2(d[0], d[1], h0, l0);
             split2(d[2], d[3], h1, l1);
             DH.put4(ro_q, 16 * st, 16 * tt, h0, h1);
@@ -867,21 +905,10 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         }
         // the states' part of dx, 16 columns of p, lanes along s
         f32x4 ax[Own::PT][Own::TT] = {};
-        auto states_of_dx = [&]() {
-#pragma unroll
-            for (int u = 0; u < Own::PT; ++u)
-#pragma unroll 4
-                for (int k = 0; k < N / 32; ++k) {
-                    const bf16x8 l = Ls.col(co_p, Own::p0(wave, u), k);
-#pragma unroll
-                    for (int t = 0; t < Own::TT; ++t)
-                        ax[u][t] = mfma(l, B.row(ro_n, 16 * (Own::t0(wave) + t), k), ax[u][t]);
-                }
-        };
         phase();
-        states_of_dx();
+        times_state<P, N, false>(Ls, Ls, B, co_p, ro_n, wave, ax);
         barrier();
-        put_part(false);
+        put_part<P, N, NC>(Ls, ro_p, wave, false, ln);
         if (wave == NW - 1 && ch - 2 >= w.c0) dt = load_dt(p, w, ch - 2);
         last_dt = s.dt[lane], last_decay = s.up[kQ - 1];
         const int have = min(kQ, p.T - ch * kQ);
@@ -889,7 +916,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
         auto make_dx = [&]() {
             const Buf out = view(oX + (int64_t)ch * kQ * sp, (int64_t)have * sp);
             const int t0 = Own::t0(wave);
-            states_of_dx();
+            times_state<P, N, false>(Ls, Ls, B, co_p, ro_n, wave, ax);
 #pragma unroll
             for (int u = 0; u < Own::PT; ++u) {
                 const int p0 = Own::p0(wave, u);
@@ -902,7 +929,7 @@ __global__ __launch_bounds__(waves<N>() * 64) void scan_walk_back(const ScanPara
 #pragma unroll
                     for (int t = 0; t < Own::TT; ++t)
                         if (t0 + t < 2 * i + 2) {
-                            a[t] = mfma(yt, ML.row(ro_q, 16 * (t0 + t), i), a[t]);
+                            a[t] = mfma(yt, second(t0 + t, i).row(ro_q, 32 + 16 * ((t0 + t) & 1), 0), a[t]);
                             a[t] = mfma(yt, M.row(ro_q, 16 * (t0 + t), i), a[t]);
                         }
                 }
@@ -1084,13 +1111,9 @@ constexpr size_t lds_segments() {
     return 2 * sizeof(Scalars) + (Rows<N>::ELEMS + Rows<P>::ELEMS) * 2;
 }
 template <int P, int N>
-constexpr size_t lds_forward() {
-    return 2 * sizeof(Scalars) + (2 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + Rows<P>::ELEMS + 2 * N * P) * 2;
-}
-template <int P, int N>
 constexpr size_t lds_backward() {
     return 2 * sizeof(Scalars) + 2 * sizeof(Sums) + sizeof(Ends<N>) +
-           (4 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + 2 * Rows<P>::ELEMS + N * P) * 2;
+           (3 * Rows<kQ>::ELEMS + 2 * Rows<N>::ELEMS + 2 * Rows<P>::ELEMS + N * P) * 2;
 }
 unsigned sub_grid(const ScanParams &p) { return (unsigned)(p.nseq * p.H * p.parts * p.nsub); }
 unsigned fold_grid(const ScanParams &p) {
@@ -1118,7 +1141,7 @@ hipError_t launch(unsigned grid, unsigned threads, size_t lds, hipStream_t s, co
 
 template <int P, int N>
 hipError_t forward(const ScanParams &p, bool keep, hipStream_t s) {
-    static_assert(lds_backward<P, N>() <= 160 * 1024 && lds_forward<P, N>() <= 160 * 1024, "LDS of a compute unit");
+    static_assert(lds_backward<P, N>() <= 160 * 1024 && lds_forward<P, N>(places<P, N>()) <= 160 * 1024, "LDS of a compute unit");
     const unsigned grid = (unsigned)(p.nseq * p.H * p.parts * p.nseg), th = waves<N>() * 64;
     hipError_t e = hipSuccess;
     if (p.nseg > 1) {
@@ -1126,8 +1149,8 @@ hipError_t forward(const ScanParams &p, bool keep, hipStream_t s) {
         if (e == hipSuccess) e = launch<scan_fold<false>>(fold_grid(p), 256, 0, s, p);
     }
     if (e != hipSuccess) return e;
-    return keep ? launch<scan_walk<P, N, true>>(grid, th, lds_forward<P, N>(), s, p)
-                : launch<scan_walk<P, N, false>>(grid, th, lds_forward<P, N>(), s, p);
+    return keep ? launch<scan_walk<P, N, true>>(grid, th, lds_forward<P, N>(places<P, N>()), s, p)
+                : launch<scan_walk<P, N, false>>(grid, th, lds_forward<P, N>(places<P, N>()), s, p);
 }
 template <int P, int N>
 hipError_t backward(const ScanParams &p, hipStream_t s) {
