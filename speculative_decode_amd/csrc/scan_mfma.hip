@@ -32,7 +32,7 @@
 // split into three bf16 parts (all 24 bits) wherever a state or the gradient of a decay
 // depends on them: an entry of dA is a long sum of terms of either sign, and two parts left
 // it 1e-6 to 4e-6 off.  What only outputs in bf16 depend on is split in two parts (16 bits): the pair
-// weights, and the states in y and dx.  (In one part the walks were 8 and 10 % faster, but y and
+// weights, and the states in y and dx.  (In one part the walks were 7 and 10 % faster, but y and
 // dx after a few tokens from a given state 1.4 times as far off as their own rounding.)  dB and dC per
 // head are kept to the upper 24 bits of fp32, 16 of them significant, until the group's are summed
 // (rounded to bf16 there, the sum was off by 1.4 to 1.6 times its own rounding).
@@ -521,16 +521,9 @@ __device__ __forceinline__ void times_state(const Rows<P> &h, const Rows<P> &low
 }
 
 // ---------------------------------------------------------------- forward
-// KEEP: leave the state entering each chunk behind for the backward walk, as the tiles it is held
-// in: [n tile][p tile][lane][4].
-// 8192 tokens, 32 heads of 128 x 128 (60 GFLOP with its backward call): 112 us, 123 with the
-// states left behind (456 MB at 3.7 TB/s; unit by unit LDS 50 %, vector ALU 43 %, matrix cores
-// 22 % busy).  What bounds it is that a chunk's phases follow one another: with 131 KB of LDS one
-// workgroup of two waves a SIMD has the compute unit.  (Narrower walks, two of which fit, would
-// read B and C and form the pairs once more each; not measured.)
 // The state's two parts have a place in LDS each, or take one in turn, the second first, where a compute unit
 // then has room for one workgroup more.  In turn costs a barrier a chunk and reads B and C once for each
-// part: 8192 tokens, 32 heads of 128 x 128, where nothing is won, 135 us against 123; 16 sequences of 1024 tokens,
+// part: 8192 tokens, 32 heads of 128 x 128, where nothing is won, 135 us against 122; 16 sequences of 1024 tokens,
 // 32 heads of 64 x 128, without states left behind, 131 us against 147.
 template <int P, int N>
 constexpr size_t lds_forward(int places) {
@@ -547,14 +540,24 @@ template <int P, int N>
 constexpr int places() {
     return groups<P, N>(1) > groups<P, N>(2) ? 1 : 2;
 }
+
+// KEEP: leave the state entering each chunk behind for the backward walk, as the tiles it is held
+// in: [n tile][p tile][lane][4].
+// 8192 tokens, 32 heads of 128 x 128 (60 GFLOP with its backward call): 113 us, 122 with the
+// states left behind (456 MB at 3.7 TB/s; unit by unit LDS 49 %, vector ALU 44 %, matrix cores
+// 22 % busy).  What bounds it is that a chunk's phases follow one another: with 131 KB of LDS one
+// workgroup of two waves a SIMD has the compute unit.  (Narrower walks, two of which fit, would
+// read B and C and form the pairs once more each; not measured.)
 template <int P, int N, bool KEEP>
-__global__ __launch_bounds__(waves<N>() * 64, (waves<N>() / 4 * groups<P, N>(places<P, N>()))) void scan_walk(const ScanParams p) {
+__global__ __launch_bounds__(waves<N>() * 64, (waves<N>() / 4 * groups<P, N>(places<P, N>()))) void scan_walk(
+    const ScanParams p) {
     constexpr bool TURN = places<P, N>() == 1;
     constexpr int NW = waves<N>(), TH = NW * 64, NC = (N / 16 + NW - 1) / NW;
     typedef Tiles<P, N> Own;
     extern __shared__ __align__(16) char lds[];
     Scalars *sc = reinterpret_cast<Scalars *>(lds);
-    const Rows<kQ> M{reinterpret_cast<bf16 *>(sc + 2)}, ML{M.p + Rows<kQ>::ELEMS};  // pair weights in two parts: row t, column s
+    // pair weights in two parts: row t, column s
+    const Rows<kQ> M{reinterpret_cast<bf16 *>(sc + 2)}, ML{M.p + Rows<kQ>::ELEMS};
     const Rows<N> B{ML.p + Rows<kQ>::ELEMS}, C{B.p + Rows<N>::ELEMS};
     const Rows<P> X{C.p + Rows<N>::ELEMS};
     const Rows<P> Hs{X.p + Rows<P>::ELEMS}, Hl{TURN ? Hs.p : Hs.p + N * P};  // the state's parts, row n
@@ -702,10 +705,10 @@ struct Ends {
     float dot[8];
 };
 
-// 8192 tokens, 32 heads of 128 x 128: 265 us, 723 MB at 2.7 TB/s; LDS 52 %, vector ALU 50 %
-// and matrix cores 23 % busy, as in the walk forward one after another; 31700 cycles a chunk, of
+// 8192 tokens, 32 heads of 128 x 128: 259 us, 723 MB at 2.8 TB/s; LDS 51 %, vector ALU 49 %
+// and matrix cores 23 % busy, as in the walk forward one after another; 31800 cycles a chunk, of
 // which the matrix products alone need 7200.  4 sequences of up to 2001 tokens, 32 heads of
-// 128 x 256 in two parts each: 597 us, 1.57 GB at 2.6 TB/s (chunks behind a sequence's end are walked
+// 128 x 256 in two parts each: 596 us, 1.57 GB at 2.6 TB/s (chunks behind a sequence's end are walked
 // like any other, on zeros).  (Two parts instead of three behind the states and dA took 11 us less
 // at an earlier stage, but left dA 1e-6 off and more.)
 template <int P, int N>
@@ -1141,7 +1144,8 @@ hipError_t launch(unsigned grid, unsigned threads, size_t lds, hipStream_t s, co
 
 template <int P, int N>
 hipError_t forward(const ScanParams &p, bool keep, hipStream_t s) {
-    static_assert(lds_backward<P, N>() <= 160 * 1024 && lds_forward<P, N>(places<P, N>()) <= 160 * 1024, "LDS of a compute unit");
+    constexpr size_t lds = lds_forward<P, N>(places<P, N>());
+    static_assert(lds <= 160 * 1024 && lds_backward<P, N>() <= 160 * 1024, "LDS of a compute unit");
     const unsigned grid = (unsigned)(p.nseq * p.H * p.parts * p.nseg), th = waves<N>() * 64;
     hipError_t e = hipSuccess;
     if (p.nseg > 1) {
@@ -1149,8 +1153,8 @@ hipError_t forward(const ScanParams &p, bool keep, hipStream_t s) {
         if (e == hipSuccess) e = launch<scan_fold<false>>(fold_grid(p), 256, 0, s, p);
     }
     if (e != hipSuccess) return e;
-    return keep ? launch<scan_walk<P, N, true>>(grid, th, lds_forward<P, N>(places<P, N>()), s, p)
-                : launch<scan_walk<P, N, false>>(grid, th, lds_forward<P, N>(places<P, N>()), s, p);
+    return keep ? launch<scan_walk<P, N, true>>(grid, th, lds, s, p)
+                : launch<scan_walk<P, N, false>>(grid, th, lds, s, p);
 }
 template <int P, int N>
 hipError_t backward(const ScanParams &p, hipStream_t s) {
@@ -1193,7 +1197,7 @@ hipError_t by_shape(int P, int N, F f) {
 }  // namespace
 
 // Against the general kernels, bf16, 32 heads of 128 x 128, all kernels of forward and backward:
-// 1024 tokens 113 us against 390, 8192 tokens 545 against 3190.  (P or N of 16 would leave half of
+// 1024 tokens 117 us against 390, 8192 tokens 537 against 3190.  (P or N of 16 would leave half of
 // every operand's inner indices empty.)
 bool scan_mfma_supported(const ScanParams &p) {
     // (the last: a chunk's rows, of up to 4 parts of a head, stay within the 2 GiB of a bounded view)
@@ -1201,9 +1205,9 @@ bool scan_mfma_supported(const ScanParams &p) {
 }
 // Segments: as many as fill the chip with one workgroup per compute unit, but none shorter
 // than two chunks (the launch that prepares them walks every segment but one).  8192 tokens, 32
-// heads of 128 x 128: walk back 1602 us in one segment, 810 in two, 422 in four, 266 in eight; walk
-// forward 701, 353, 189, 123; the preparing launch 71 us in two segments, 41 in four and in eight,
-// with its fold 76, 48 and 53 each way.
+// heads of 128 x 128: walk back 1599 us in one segment, 808 in two, 422 in four, 265 in eight; walk
+// forward 708, 357, 192, 124; the preparing launch 71 us in two segments, 43 in four and 42 in eight,
+// with its fold 76, 49 and 54 each way.
 void scan_mfma_cut(ScanParams &p) {
     p.nch = (p.T + kQ - 1) / kQ;
     p.parts = p.P / columns(p.P, p.N);
@@ -1214,7 +1218,7 @@ void scan_mfma_cut(ScanParams &p) {
     p.segc = (p.nch + n - 1) / n;
     p.nseg = (p.nch + p.segc - 1) / p.segc;
     // halves where they are long enough to be worth the larger fold (8 chunks and more: 8192
-    // tokens of 32 heads 46 -> 41 us against 8.5 -> 12 us; at 2 chunks, 1024 tokens, 11.7 -> 13.3
+    // tokens of 32 heads 47 -> 42 us against 8.5 -> 12 us; at 2 chunks, 1024 tokens, 11.7 -> 13.3
     // and 8.3 -> 11.4)
     p.subc = p.segc % 2 == 0 && p.segc >= 8 ? p.segc / 2 : p.segc;
     p.nsub = (p.nch + p.subc - 1) / p.subc;

@@ -601,7 +601,9 @@ __device__ __forceinline__ void take_out(u32x4 &raw, const Spot &spot, int j) {
             if (place == i) {
                 constexpr int per = BF ? 2 : 1;
                 const uint32_t w = raw[i / per];
-                const uint32_t out = !BF ? 0xff800000u : i % per ? (w & 0xffffu) | 0xff800000u : (w & 0xffff0000u) | 0xff80u;
+                const uint32_t out = !BF ? 0xff800000u
+                                     : i % per ? (w & 0xffffu) | 0xff800000u
+                                               : (w & 0xffff0000u) | 0xff80u;
                 raw[i / per] = mine ? out : w;
             }
     });
